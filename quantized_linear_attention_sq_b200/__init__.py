@@ -2,7 +2,8 @@
 (GDN and KDA), B200-native.
 
 ``StatePool`` (state.py) is the torch-facing handle over the C ABI in
-include/sq.h; ``_abi`` is the raw ctypes binding; ``synth`` draws seeded
+include/sq.h; ``ragged`` has the tables and the query/key norm of ragged
+batches (include/sq_ragged.h); ``_abi`` is the raw ctypes binding; ``synth`` draws seeded
 synthetic workloads. The compute runs in libsq.so (csrc/), built in-tree by
 ``build.py`` for sm_100a.
 """

@@ -32,6 +32,17 @@ SQ_STATUS_BAD_SLOT = 4
 SQ_STATUS_TIMEOUT = 8
 SQ_STATUS_WINDOW = 16
 
+SQ_STATUS_TRUNCATED = 32
+SQ_STATUS_NO_SLOT = 64
+
+SQ_F32 = 0
+SQ_BF16 = 1
+SQ_F16 = 2
+SQ_NORM_L2 = 0
+SQ_NORM_RMS = 1
+SQ_RAGGED_BLOCK = 64
+SQ_RAGGED_MAX_REQUESTS = 16384
+
 SQ_NOALLOC_MAX_HEADS = 64
 
 
@@ -66,6 +77,16 @@ class CalibOut(ctypes.Structure):
     _fields_ = [("unit_bits", ctypes.c_void_p), ("pivot_mask", ctypes.c_void_p), ("col_scale", ctypes.c_void_p),
                 ("row_impact", ctypes.c_void_p), ("unit_sigma2", ctypes.c_void_p),
                 ("unit_weight", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("eps", ctypes.c_float), ("q_scale", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("base", ctypes.c_double)]
+
+
+class RaggedTables(ctypes.Structure):
+    _fields_ = [("cu_seqlens", ctypes.c_void_p), ("cu_blocks", ctypes.c_void_p), ("block_req", ctypes.c_void_p),
+                ("past", ctypes.c_void_p)]
 
 
 _lib = None
@@ -112,10 +133,17 @@ def lib() -> ctypes.CDLL:
     L.sq_calib_free.argtypes = [P]
     L.sq_window_step.argtypes = [P, P, P, I32, P, P, P, P, P, P, P, I32, P]
     L.sq_window_buffer_bytes.argtypes = [P, I32, ctypes.POINTER(U64), ctypes.POINTER(U64)]
+    I64 = ctypes.c_int64
+    L.sq_batch_tables.argtypes = [P, P, I32, I32, P, P, P, P, P, P, I32, P, P, P, P]
+    L.sq_qk_norm.argtypes = [ctypes.POINTER(NormDesc), P, P, I64, I64, I32, P, P, P, P, P, I32, I32, P, I32, I32, I32, P]
+    L.sq_ragged_workspace_bytes.argtypes = [P, I32, I32, I32, I32, ctypes.POINTER(U64)]
+    L.sq_prefill_ragged.argtypes = ([P] * 5 + [I64] * 3 + [I32] + [P] * 3 + [ctypes.POINTER(RaggedTables), P, I32, I32,
+                                    I32, P, U64, P])
     for name in ("sq_state_alloc", "sq_state_free", "sq_quantize_state", "sq_decode_step",
                  "sq_dequantize_state", "sq_state_bytes", "sq_head_layout", "sq_get_status",
                  "sq_prefill", "sq_decode_step_host", "sq_calib_allocate", "sq_calib_begin", "sq_calib_add_states", "sq_calib_add_tokens", "sq_calib_finish",
-                 "sq_calib_free", "sq_window_step", "sq_window_buffer_bytes"):
+                 "sq_calib_free", "sq_window_step", "sq_window_buffer_bytes", "sq_batch_tables", "sq_qk_norm",
+                 "sq_ragged_workspace_bytes", "sq_prefill_ragged"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -171,6 +199,30 @@ def sq_window_buffer_bytes(h, W: int):
 
 def sq_prefill(h, pool, S0, q, k, v, beta, g, o, S_out, lengths, slot_ids, B, L, stream) -> None:
     check(lib().sq_prefill(h, pool, S0, q, k, v, beta, g, o, S_out, lengths, slot_ids, B, L, stream))
+
+
+def sq_batch_tables(lengths, past, B, max_rows, cu_seqlens, cu_blocks, positions, block_req, slot_ids, used, n_slots,
+                    slot_out, used_out, status, stream) -> None:
+    check(lib().sq_batch_tables(lengths, past, B, max_rows, cu_seqlens, cu_blocks, positions, block_req, slot_ids,
+                                used, n_slots, slot_out, used_out, status, stream))
+
+
+def sq_qk_norm(desc: NormDesc, q, k, q_row_stride, k_row_stride, in_dtype, q_weight, k_weight, positions, q_out, k_out,
+               out_dtype, rows, n_rows, h_q, h_k, d, stream) -> None:
+    check(lib().sq_qk_norm(ctypes.byref(desc), q, k, q_row_stride, k_row_stride, in_dtype, q_weight, k_weight,
+                           positions, q_out, k_out, out_dtype, rows, n_rows, h_q, h_k, d, stream))
+
+
+def sq_ragged_workspace_bytes(h, dtype: int, B: int, rows: int, max_len: int) -> int:
+    n = ctypes.c_uint64()
+    check(lib().sq_ragged_workspace_bytes(h, dtype, B, rows, max_len, ctypes.byref(n)))
+    return n.value
+
+
+def sq_prefill_ragged(h, pool, q, k, v, q_stride, k_stride, v_stride, dtype, beta, g, o, tables: RaggedTables,
+                      slot_ids, B, rows, max_len, workspace, workspace_bytes, stream) -> None:
+    check(lib().sq_prefill_ragged(h, pool, q, k, v, q_stride, k_stride, v_stride, dtype, beta, g, o,
+                                  ctypes.byref(tables), slot_ids, B, rows, max_len, workspace, workspace_bytes, stream))
 
 
 def sq_dequantize_state(h, pool, S_out, slot_ids, B, stream) -> None:

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "sq.h"
+#include "sq_handle.h"
 #include "sq_host.h"
 #include "sq_kernels.cuh"
 #include "sq_prefill.cuh"
@@ -65,49 +66,7 @@ inline float clip_ratio(float phi) { return phi < 1.0f ? phi : 1.0f; }
 // unchanged).
 constexpr int kStepChunk = 1;
 
-// Limit of the kernels' bounded waits (a stage's data, the partials buffer).
-constexpr uint64_t kWaitNs = 2000000000ull;
-
 }  // namespace
-
-struct sq_handle {
-  sq_state_desc desc{};
-  int d = 0;
-  int device = 0;
-  int num_sms = 0;
-  // host copies of the layout
-  std::vector<uint32_t> rec_off, rec_bytes;
-  std::vector<uint16_t> row_off;
-  std::vector<uint8_t> row_code;
-  uint64_t slot_bytes = 0, pool_bytes = 0, max_rec = 0;
-  // device tables (one allocation)
-  void* dev_block = nullptr;
-  sqk::Tables tables{};
-  // launch configuration of the step kernel
-  int step_grid = 0;
-  int nstage = 0;
-  uint32_t rec_cap = 0, stage_bytes = 0;
-  uint64_t stage_rec = 0;  // largest record that goes through a stage
-  size_t step_smem = 0;
-  uint64_t launches = 0;
-  uint64_t wait_ns = kWaitNs;     // limit of the kernels' bounded waits
-  uint32_t test_extra_tx = 0;     // testing only (sq_test_stall_stage)
-  // sq_decode_step_host: two device staging sets used in turn, the internal
-  // stream their host-to-device copies run on, and the events that order
-  // the copies after the step that last read a set.
-  struct HostStage {
-    void* block = nullptr;
-    int32_t cap_B = 0;
-    cudaEvent_t copied = nullptr;  // the set's inputs are on the device
-    cudaEvent_t read = nullptr;    // the step that used the set has run
-  };
-  HostStage host_stage[2];
-  cudaStream_t copy_stream = nullptr;
-  uint64_t host_calls = 0;
-  // sq_window_step: launch plan of the last window length used
-  int win_W = 0, win_grid = 0;
-  uint32_t win_smem = 0;
-};
 
 namespace {
 
@@ -1090,7 +1049,7 @@ extern "C" sq_status sq_decode_step_noalloc(const sq_state_desc* desc, const sq_
   a.slots = slot_ids;
   a.B = B; a.h_v = hv; a.h_k = desc->h_k; a.n_slots = desc->n_slots; a.gate_kind = desc->gate;
   a.slot_bytes = off;
-  a.wait_ns = kWaitNs;
+  a.wait_ns = sqi::kWaitNs;
   a.test_extra_tx = 0;
   a.t.rec_off = reinterpret_cast<const uint32_t*>(nd->scratch + o_rec_off);
   a.t.rec_bytes = reinterpret_cast<const uint32_t*>(nd->scratch + o_rec_bytes);

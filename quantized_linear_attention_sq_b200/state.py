@@ -51,6 +51,24 @@ def _host_ptr(t: torch.Tensor | None, dtype, name, numel) -> int | None:
     return t.data_ptr()
 
 
+DTYPES = {torch.float32: _abi.SQ_F32, torch.bfloat16: _abi.SQ_BF16, torch.float16: _abi.SQ_F16}
+
+
+def row_ptr(t: torch.Tensor, dtype, name, shape, device):
+    """(address, row stride in elements) of a [rows, heads, d] tensor whose
+    rows may lie apart (a column slice of a wider matrix)."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, heads, d = shape
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else heads * d
+
+
 class StatePool:
     """A layer's recurrent-state pool handle (calibration tables on device).
 
@@ -179,6 +197,49 @@ class StatePool:
                         _ptr(S_out, torch.float32, "S_out", B * hv * d * d),
                         _ptr(lengths, torch.int32, "lengths", B), _ptr(slot_ids, torch.int32, "slot_ids", B),
                         B, L, _stream(stream))
+
+    def ragged_workspace_bytes(self, B: int, rows: int, max_len: int | None = None, dtype=torch.bfloat16) -> int:
+        """Bytes of workspace prefill_ragged needs for a batch of these sizes."""
+        return _abi.sq_ragged_workspace_bytes(self._h, DTYPES[dtype], int(B), int(rows),
+                                              int(rows if max_len is None else max_len))
+
+    def new_ragged_workspace(self, B: int, rows: int, max_len: int | None = None, dtype=torch.bfloat16) -> torch.Tensor:
+        """A workspace for prefill_ragged; calls that may overlap need one each."""
+        return torch.empty(self.ragged_workspace_bytes(B, rows, max_len, dtype), dtype=torch.uint8,
+                           device=self.device)
+
+    def prefill_ragged(self, pool, q, k, v, beta, g, o, tables, slot_ids=None, max_len=None, workspace=None,
+                       stream=None):
+        """The gated delta rule over a ragged batch (sq_prefill_ragged): q, k
+        [rows, h_k, d], v, o [rows, h_v, d] (bf16, fp16 or fp32; q, k and v may
+        be column slices of wider matrices), beta [rows, h_v], g [rows, h_v]
+        or [rows, h_v, d], tables a ragged.BatchTables. A request with
+        past > 0 goes on from its slot's state, another starts from zeros."""
+        B, rows, d, hv, hk = tables.cu_seqlens.numel() - 1, q.shape[0], self.d, self.h_v, self.h_k
+        if q.dtype not in DTYPES:
+            raise ValueError(f"q must be one of {tuple(DTYPES)}, got {q.dtype}")
+        if tables.cu_blocks.numel() != B + 1 or tables.block_req.numel() < rows // _abi.SQ_RAGGED_BLOCK + B:
+            raise ValueError("cu_blocks or block_req is too short for the batch")
+        gn = rows * hv * (d if self.gate_kind == _abi.SQ_GATE_KEY_CHANNEL else 1)
+        max_len = rows if max_len is None else int(max_len)
+        need = self.ragged_workspace_bytes(B, rows, max_len, q.dtype)
+        with torch.cuda.device(self.device):
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                if isinstance(stream, torch.cuda.Stream):
+                    workspace.record_stream(stream)
+            i32 = torch.int32
+            t = _abi.RaggedTables(_ptr(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
+                                  _ptr(tables.cu_blocks, i32, "cu_blocks", B + 1),
+                                  _ptr(tables.block_req, i32, "block_req"), _ptr(tables.past, i32, "past", B))
+            qp, qs = row_ptr(q, q.dtype, "q", (rows, hk, d), self.device)
+            kp, ks = row_ptr(k, q.dtype, "k", (rows, hk, d), self.device)
+            vp, vs = row_ptr(v, q.dtype, "v", (rows, hv, d), self.device)
+            _abi.sq_prefill_ragged(self._h, self._check_pool(pool), qp, kp, vp, qs, ks, vs, DTYPES[q.dtype],
+                                   _ptr(beta, torch.float32, "beta", rows * hv), _ptr(g, torch.float32, "g", gn),
+                                   _ptr(o, q.dtype, "o", rows * hv * d), t, _ptr(slot_ids, i32, "slot_ids", B), B,
+                                   rows, max_len, _ptr(workspace, torch.uint8, "workspace"),
+                                   workspace.numel() if workspace is not None else 0, _stream(stream))
 
     def dequantize_state(self, pool, S_out, slot_ids=None, stream=None):
         B = S_out.shape[0]
