@@ -1,0 +1,429 @@
+// sq_chunk_scan.cuh -- the gated delta rule in blocks of 64 rows, second
+// kernel: the walk over a request's blocks (see sq_chunk_prepare.cuh for the
+// formulas and for T and P T).
+//
+// One CTA per (request, value head), one per SM. The transposed state S^T
+// [128 value columns][128 key rows] lives in registers in fp32 (a thread owns
+// one value column and half of the key rows) and all four products of a block
+// run on the tensor cores with a transposed left operand out of tensor
+// memory, so no operand that a thread computes ever goes through shared
+// memory:
+//     D1 = S^T [k; q]^T         (A: S^T,  B: the k and q tiles as TMA left them)
+//     D2 = r^T [T; P T]^T       (A: r^T,  B: the prepared block)
+//     D3 = (e^(G63 - G) u)^T k  (A: u^T,  B: the k tile again, read the other way)
+// with r = v - e^G D1k, u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
+// fp32 by the threads. S, r and u are split into three bf16 terms (T and P T
+// are stored so), k and q are bf16 already: D1 and D3 take three products,
+// D2 the six largest of nine, smallest first, so that every result is
+// fp32-accurate. The state adds one fresh accumulator per block in fp32:
+// the tensor core never accumulates across blocks.
+//
+// Ten warps: eight compute (two per 32 lanes of tensor memory, sharing the
+// columns), one issues the TMA loads of the next block, one the matrix
+// products. The chain of a block is D1k -> r -> D2u -> u -> D3 -> S; the q
+// product runs under r, the P T product and o under u and D3.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "sq_chunk_prepare.cuh"
+
+namespace sqr {
+
+constexpr int kScanCompute = 256;             // threads that own a part of the state
+constexpr int kScanThreads = kScanCompute + 64;
+constexpr int kScanStages = 2;
+constexpr uint32_t kTileBytes = 64 * 128 * 2;  // q, k or v rows of a block
+constexpr uint32_t kStageBytes = 3 * kTileBytes + (kPrepBytes + 1023) / 1024 * 1024;
+constexpr uint32_t kStageTx = 3 * kTileBytes + kPrepBytes;
+
+struct ScanCtl {
+  uint64_t full[kScanStages], empty[kScanStages];
+  uint64_t s_ready, r_ready, u_ready, d1, d2, d2o, d3, drain;
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr size_t kScanSmem = 1024 + kScanStages * kStageBytes + sizeof(ScanCtl) + 16;
+
+struct ScanArgs {
+  PrepArgs p;
+  uint64_t wait_ns;
+};
+
+// Columns of tensor memory (512, all of it).
+constexpr uint32_t TM_S = 0;      // S^T terms: hi and mid of key rows 0..63, of 64..127, then lo; D3 takes 0..127
+constexpr uint32_t TM_U = 128;    // u^T terms (over the lo terms of S^T)
+constexpr uint32_t TM_R = 224;    // r^T terms
+constexpr uint32_t TM_D1K = 320;  // S^T k^T, then D2u
+constexpr uint32_t TM_D1Q = 384;
+constexpr uint32_t TM_D2O = 448;
+
+// Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
+__device__ __forceinline__ uint32_t s_col(int s, int ks) {
+  return s == 2 ? 128u + 8u * ks : 64u * (ks >> 2) + 32u * s + 8u * (ks & 3);
+}
+
+// ---------------------------------------------------------- instructions
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          sqk::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(sqk::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The barrier gets one arrival when every product issued so far is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sqk::smem_u32(bar))
+               : "memory");
+}
+// D (+)= A B, A [128 x 16] bf16 in tensor memory, B in shared memory.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#define SQ_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define SQ_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+__device__ __forceinline__ void tc_ld32(uint32_t (&x)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : SQ_R8(x, 0), SQ_R8(x, 8), SQ_R8(x, 16), SQ_R8(x, 24)
+      : "r"(addr)
+      : "memory");
+}
+// Waits for the loads; the values pass through it, so no use of them moves above.
+#define SQ_RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SQ_RW8(x, 0), SQ_RW8(x, 8), SQ_RW8(x, 16), SQ_RW8(x, 24)::"memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      SQ_W8(x, 0), SQ_W8(x, 8)
+      : "memory");
+}
+
+// fp32 accumulators, bf16 operands, M = 128, N columns; `mn`: B has N contiguous.
+__host__ __device__ constexpr uint32_t mma_desc(uint32_t N, bool mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Shared memory operand: address, leading and stride offsets in bytes, swizzle mode (0 none, 2: 128 bytes).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+         (1ull << 46) | (swizzle << 61);
+}
+
+// 32 fp32 values of a lane (k index 0..31 of an A operand) to tensor memory as three terms.
+template <typename Col>
+__device__ __forceinline__ void put_terms(const float (&x)[32], uint32_t base, Col col) {
+  uint32_t t[kTerms][16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t w[kTerms];
+    split3(x[2 * i], x[2 * i + 1], w);
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
+  }
+#pragma unroll
+  for (int s = 0; s < kTerms; ++s) tc_st16(base + col(s), t[s]);
+}
+
+// A warp's arrival on a barrier once its tensor memory stores are done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  tc_wait_st();
+  tc_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) sqk::mbar_arrive(bar);
+}
+
+// Wait of a whole warp; false: it ran out, in any lane.
+__device__ __forceinline__ bool warp_wait(ScanCtl& c, uint64_t* bar, uint32_t parity, uint64_t ns) {
+  const bool ok = sqk::mbar_wait_bounded(bar, parity, ns);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  c.abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kScanCompute) : "memory"); }
+
+template <bool PACKED>
+__global__ void __launch_bounds__(kScanThreads, 1)
+    k_chunk_scan(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const ScanArgs args) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  ScanCtl& ctl = *reinterpret_cast<ScanCtl*>(smem + kScanStages * kStageBytes);
+  const RaggedArgs& a = args.p.r;
+  const int b = blockIdx.x / a.h_v, h = blockIdx.x - b * a.h_v, hk = h / (a.h_v / a.h_k);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int first, n;
+  ragged_span(a, b, first, n);
+  if (n < a.min_long) return;
+  const int slot = a.slots ? a.slots[b] : b;
+  const int blocks = (n + 63) >> 6, c0 = args.p.cu_blocks[b];
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
+  if (slot < 0 || slot >= a.n_slots || c0 < 0 || c0 + blocks > args.p.n_blocks) {
+    for (int x = tid; x < n * 16; x += kScanThreads)
+      reinterpret_cast<uint4*>(out + ((size_t)(first + (x >> 4)) * a.h_v + h) * 128)[x & 15] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) atomicOr(a.t.status, ST_SLOT);
+    return;
+  }
+  const bool resume = a.past && a.past[b] > 0;
+  uint8_t* record = a.pool + (uint64_t)slot * a.slot_bytes + (PACKED ? a.t.rec_off[h] : 0u);
+  float* S_pool = reinterpret_cast<float*>(a.pool) + ((size_t)slot * a.h_v + h) * 128 * 128;
+
+  if (tid == 0) {
+    for (int x = 0; x < kScanStages; ++x) {
+      sqk::mbar_init(&ctl.full[x], 1);
+      sqk::mbar_init(&ctl.empty[x], kScanCompute / 32);
+    }
+    sqk::mbar_init(&ctl.s_ready, kScanCompute / 32);
+    sqk::mbar_init(&ctl.r_ready, kScanCompute / 32);
+    sqk::mbar_init(&ctl.u_ready, kScanCompute / 32);
+    sqk::mbar_init(&ctl.d1, 1);
+    sqk::mbar_init(&ctl.d2, 1);
+    sqk::mbar_init(&ctl.d2o, 1);
+    sqk::mbar_init(&ctl.d3, 1);
+    sqk::mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    sqk::fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sqk::smem_u32(&ctl.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // S^T: value column of this thread's lane, key rows 64 half .. 64 half + 63
+  const int half = warp >> 2, col = (warp & 3) * 32 + lane;  // compute warps
+  float S[2][32];
+  if (warp < 8) {
+    const float* src = S_pool + (size_t)(64 * half) * 128 + col;
+    if (PACKED && resume) {
+      float* Ssh = reinterpret_cast<float*>(smem);
+      unpack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
+      src = Ssh + (64 * half) * 128 + col;
+    }
+#pragma unroll
+    for (int x = 0; x < 64; ++x) S[x >> 5][x & 31] = resume ? src[x * 128] : 0.0f;
+    if (PACKED && resume) sqk::fence_proxy_async_smem();  // before TMA writes where S was read
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tm = ctl.tmem;
+  const uint64_t ns = args.wait_ns;
+  uint32_t st = 0;
+
+  if (warp == 8) {  // ---------------------------------------------- loads
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = 0; i < blocks; ++i) {
+        const int sg = i & 1;
+        if (i >= kScanStages && !sqk::mbar_wait_bounded(&ctl.empty[sg], ((i >> 1) - 1) & 1, ns)) {
+          ctl.abort = 1;
+          break;
+        }
+        uint8_t* stage = smem + sg * kStageBytes;
+        sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx);
+        const int row = first + 64 * i;
+        tma_tile(stage + kTileBytes, &k_map, 0, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kTileBytes + kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
+        tma_tile(stage + 2 * kTileBytes, &v_map, 0, h, row, &ctl.full[sg]);
+        sqk::bulk_g2s(stage + 3 * kTileBytes, args.p.ws + ((uint64_t)(c0 + i) * a.h_v + h) * kPrepBytes, kPrepBytes,
+                      &ctl.full[sg]);
+        tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kTileBytes / 2, &q_map, 64, hk, row, &ctl.full[sg]);
+        issued = i + 1;
+      }
+      // no copy is in flight when the CTA ends
+      for (int i = max(0, issued - kScanStages); i < issued; ++i)
+        sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
+    }
+  } else if (warp == 9) {  // ------------------------------------- products
+    if (lane == 0) {
+      const uint32_t d64 = mma_desc(64, false), d128 = mma_desc(128, true);
+      for (int i = 0; i < blocks; ++i) {
+        const int sg = i & 1;
+        const uint32_t ph = i & 1;
+        const uint32_t stage = sqk::smem_u32(smem) + sg * kStageBytes;
+        const uint32_t qt = stage, kt = stage + kTileBytes, prep = stage + 3 * kTileBytes;
+        if (!sqk::mbar_wait_bounded(&ctl.full[sg], (i >> 1) & 1, ns) || !sqk::mbar_wait_bounded(&ctl.s_ready, ph, ns)) break;
+        tc_after();
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t tile = which ? qt : kt, d = tm + (which ? TM_D1Q : TM_D1K);
+#pragma unroll
+          for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma(d, tm + TM_S + s_col(s, ks),
+                     smem_desc(tile + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16, 1024, 2), d64,
+                     s < kTerms - 1 || ks > 0);
+          if (which == 0) tc_commit(&ctl.d1);
+        }
+        if (!sqk::mbar_wait_bounded(&ctl.r_ready, ph, ns)) break;
+        tc_after();
+        constexpr int pr[6] = {2, 0, 1, 1, 0, 0}, pt[6] = {0, 2, 1, 0, 1, 0};  // terms of r and of T, smallest first
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t m = prep + which * kTerms * kTriBytes, d = tm + (which ? TM_D2O : TM_D1K);
+#pragma unroll
+          for (int x = 0; x < 6; ++x)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15
+              tc_mma(d + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
+                     smem_desc(m + pt[x] * kTriBytes + tri_base(kk), 128, 256, 0), mma_desc(64 - 16 * kk, false),
+                     x > 0 || kk > 0);
+          tc_commit(which ? &ctl.d2o : &ctl.d2);
+        }
+        if (!sqk::mbar_wait_bounded(&ctl.u_ready, ph, ns)) break;
+        tc_after();
+#pragma unroll
+        for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tm + TM_S, tm + TM_U + 32 * s + 8 * ks, smem_desc(kt + ks * 2048, kTileBytes / 2, 1024, 2), d128,
+                   s < kTerms - 1 || ks > 0);
+        tc_commit(&ctl.d3);
+      }
+      tc_commit(&ctl.drain);  // no product is in flight when the tensor memory is given back
+      if (!sqk::mbar_wait_bounded(&ctl.drain, 0, ns)) ctl.abort = 1;
+    }
+  } else {  // -------------------------------------------------- the rest
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    auto put_state = [&]() {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        put_terms(S[x], tl + TM_S, [&](int s) { return s_col(s, 4 * half + 2 * x); });
+      warp_arrive(&ctl.s_ready);
+    };
+    put_state();
+    for (int i = 0; i < blocks; ++i) {
+      const int sg = i & 1;
+      const uint32_t ph = i & 1;
+      uint8_t* stage = smem + sg * kStageBytes;
+      if (!warp_wait(ctl, &ctl.full[sg], (i >> 1) & 1, ns)) break;
+      const int live = min(64, n - 64 * i);
+      if (live < 64) {
+        // rows of the k tile behind the request's last: another request's, or none's
+        for (int x = tid; x < (64 - live) * 16; x += kScanCompute)
+          *reinterpret_cast<uint4*>(stage + kTileBytes + ((x >> 3) & 1) * (kTileBytes / 2) + (live + (x >> 4)) * 128 +
+                                    (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+        sqk::fence_proxy_async_smem();
+      }
+      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + 2 * kTileBytes) + 32 * half * 128 + col;
+      const float* coef = reinterpret_cast<const float*>(stage + 3 * kTileBytes + 2 * kTerms * kTriBytes);
+      const float4* eg = reinterpret_cast<const float4*>(coef + 32 * half);
+      const float4* ed = reinterpret_cast<const float4*>(coef + 64 + 32 * half);
+      const int mine = live - 32 * half;  // live rows of this half
+      float x[32];
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = j < mine ? __bfloat162float(v[j * 128]) : 0.0f;
+      if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
+      tc_after();
+      tc_ld32(w, tl + TM_D1K + 32 * half);
+      tc_wait_ld(w);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 e = eg[j >> 2];
+        x[j] = j < mine ? fmaf(-e.x, __uint_as_float(w[j]), x[j]) : 0.0f;
+        x[j + 1] = j + 1 < mine ? fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]) : 0.0f;
+        x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
+        x[j + 3] = j + 3 < mine ? fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]) : 0.0f;
+      }
+      put_terms(x, tl + TM_R + 16 * half, [](int s) { return 32u * s; });
+      warp_arrive(&ctl.r_ready);
+
+      if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
+      tc_after();
+      tc_ld32(w, tl + TM_D1K + 32 * half);
+      tc_wait_ld(w);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 e = ed[j >> 2];
+        x[j] = e.x * __uint_as_float(w[j]);
+        x[j + 1] = e.y * __uint_as_float(w[j + 1]);
+        x[j + 2] = e.z * __uint_as_float(w[j + 2]);
+        x[j + 3] = e.w * __uint_as_float(w[j + 3]);
+      }
+      put_terms(x, tl + TM_U + 16 * half, [](int s) { return 32u * s; });
+      warp_arrive(&ctl.u_ready);
+
+      // o, under the state's product
+      if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
+      tc_after();
+      {
+        uint32_t y[32];
+        tc_ld32(w, tl + TM_D1Q + 32 * half);
+        tc_ld32(y, tl + TM_D2O + 32 * half);
+        tc_wait_ld(w);
+        tc_wait_ld(y);
+        __nv_bfloat16* op = out + ((size_t)(first + 64 * i + 32 * half) * a.h_v + h) * 128 + col;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 e4 = eg[j >> 2];
+          const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float o = fmaf(e[k], __uint_as_float(w[j + k]), __uint_as_float(y[j + k]));
+            if (j + k < mine) {
+              if (o != o) st |= ST_NAN;
+              op[(size_t)(j + k) * a.h_v * 128] = __float2bfloat16_rn(o);
+            }
+          }
+        }
+      }
+      const float g63 = coef[128];
+      if (!warp_wait(ctl, &ctl.d3, ph, ns)) break;
+      tc_after();
+      {
+        uint32_t y[32];
+        tc_ld32(w, tl + TM_S + 64 * half);
+        tc_ld32(y, tl + TM_S + 64 * half + 32);
+        tc_wait_ld(w);
+        tc_wait_ld(y);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          S[0][j] = fmaf(g63, S[0][j], __uint_as_float(w[j]));
+          S[1][j] = fmaf(g63, S[1][j], __uint_as_float(y[j]));
+        }
+      }
+      if (lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before the loads above
+      if (i + 1 < blocks) put_state();
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  if (ctl.abort) {  // the state in the pool stays as it was
+    if (tid == 0) atomicOr(a.t.status, sqk::ST_TIMEOUT);
+    return;
+  }
+  if (warp < 8) {
+    if (PACKED) {
+      float* Ssh = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int x = 0; x < 64; ++x) Ssh[(64 * half + x) * 128 + col] = S[x >> 5][x & 31];
+      st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
+    } else {
+      float* dst = S_pool + (size_t)(64 * half) * 128 + col;
+#pragma unroll
+      for (int x = 0; x < 64; ++x) dst[x * 128] = S[x >> 5][x & 31];
+    }
+    if (st) atomicOr(a.t.status, st);
+  }
+}
+
+}  // namespace sqr

@@ -6,6 +6,8 @@
 #include <cstdint>
 
 #include "sq.h"
+#include "sq_chunk_prepare.cuh"
+#include "sq_chunk_scan.cuh"
 #include "sq_handle.h"
 #include "sq_host.h"
 #include "sq_qknorm.cuh"
@@ -81,6 +83,74 @@ cudaError_t launch_rows_type(int dtype, const sqr::RaggedArgs& a, uint32_t max_r
 template <int D>
 cudaError_t launch_rows_gate(bool kda, int dtype, const sqr::RaggedArgs& a, uint32_t max_rec, cudaStream_t st) {
   return kda ? launch_rows_type<D, true>(dtype, a, max_rec, st) : launch_rows_type<D, false>(dtype, a, max_rec, st);
+}
+
+// ------------------------------------------------------------------ blocks
+// Requests of at least this many rows run in blocks on the tensor cores,
+// shorter ones row by row.
+constexpr int kMinLong = 24;
+
+bool in_blocks(const sq_handle* h, int dtype, int32_t max_len) {
+  return dtype == SQ_BF16 && h->desc.gate == SQ_GATE_HEAD && h->d == 128 && max_len >= kMinLong;
+}
+
+// Tensor map of a [rows, heads, 128] bf16 matrix: boxes of 64 rows of one
+// head, `cols` columns wide, rows behind the last read as zeros.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+sq_status row_map(CUtensorMap* m, const char* name, const void* p, int64_t stride, int heads, int32_t rows, int cols,
+                  CUtensorMapSwizzle swizzle) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return fail(SQ_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  if (rows == 1) stride = (int64_t)heads * 128;  // never used, but must be valid
+  const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, 1, 64}, one[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SQ_OK : fail(SQ_ERR_CUDA, "tensor map of %s: driver error %d", name, (int)r);
+}
+
+sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_ragged_tables& t, void* workspace,
+                        cudaStream_t st) {
+  sqr::ScanArgs a{};
+  a.p.r = r;
+  a.p.cu_blocks = t.cu_blocks;
+  a.p.block_req = t.block_req;
+  a.p.ws = static_cast<uint8_t*>(workspace);
+  a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
+  a.wait_ns = h->wait_ns;
+  CUtensorMap qm, km, vm;
+  sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (s != SQ_OK) return s;
+  cudaError_t e = cudaFuncSetAttribute(sqr::k_chunk_prepare, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(sqr::PrepSmem));
+  auto scan = r.fmt_fp32 ? sqr::k_chunk_scan<false> : sqr::k_chunk_scan<true>;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sqr::kScanSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "setting the block kernels' shared memory");
+  sqr::k_chunk_prepare<<<(unsigned)a.p.n_blocks * r.h_k, sqr::kPrepThreads, sizeof(sqr::PrepSmem), st>>>(a.p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    scan<<<r.B * r.h_v, sqr::kScanThreads, sqr::kScanSmem, st>>>(qm, km, vm, a);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, "launching the block kernels");
 }
 
 }  // namespace
@@ -194,7 +264,8 @@ sq_status sq_ragged_workspace_bytes(const sq_handle* h, int32_t dtype, int32_t B
   if (dtype < SQ_F32 || dtype > SQ_F16) return fail(SQ_ERR_INVALID_ARG, "bad element type %d", dtype);
   if (B < 0 || rows < 0 || max_len < 0)
     return fail(SQ_ERR_INVALID_ARG, "B, rows and max_len must be >= 0 (got %d, %d, %d)", B, rows, max_len);
-  *bytes = 0;
+  *bytes = in_blocks(h, dtype, max_len)
+               ? (uint64_t)(rows / SQ_RAGGED_BLOCK + B) * (uint64_t)h->desc.h_v * sqr::kPrepBytes : 0;
   return SQ_OK;
 }
 
@@ -250,6 +321,14 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   a.t = h->tables;
   const uint32_t max_rec = a.fmt_fp32 ? 0u : (uint32_t)h->max_rec;
   cudaStream_t st = as_stream(stream);
+  if (rows > 0 && in_blocks(h, dtype, max_len)) {
+    if (((int64_t)rows / SQ_RAGGED_BLOCK + B) * h->desc.h_k > (int64_t)INT32_MAX)
+      return fail(SQ_ERR_UNSUPPORTED, "too many blocks of rows");
+    a.min_long = kMinLong;
+    s = launch_blocks(h, a, *tables, workspace, st);
+    if (s != SQ_OK) return s;
+    h->launches += 2;
+  }
   if (d == 128) e = launch_rows_gate<128>(kda, dtype, a, max_rec, st);
   else if (d == 64) e = launch_rows_gate<64>(kda, dtype, a, max_rec, st);
   else e = launch_rows_gate<32>(kda, dtype, a, max_rec, st);

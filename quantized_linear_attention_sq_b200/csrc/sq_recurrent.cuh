@@ -79,8 +79,10 @@ struct RGeo {
 };
 
 // The slot's packed record, dequantized into S [D][D] in shared memory.
-template <int D>
-__device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const uint8_t* src, uint8_t* rec, float* S) {
+// `sync`: a barrier of the Geo<D>::NT threads that call it.
+template <int D, typename Sync>
+__device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const uint8_t* src, uint8_t* rec, float* S,
+                                             Sync sync) {
   using G = Geo<D>;
   static_assert(G::NT == RGeo<D>::NT, "one thread map");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -88,7 +90,7 @@ __device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const u
   const uint32_t rb = a.t.rec_bytes[h];
   for (uint32_t x = tid * 16; x < rb; x += G::NT * 16)
     *reinterpret_cast<uint4*>(rec + x) = *reinterpret_cast<const uint4*>(src + x);
-  __syncthreads();
+  sync();
   const float* col = a.t.col + (size_t)h * D + 16 * cc;
 #pragma unroll
   for (int r = 0; r < G::RPT; ++r) {
@@ -102,13 +104,14 @@ __device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const u
       reinterpret_cast<float2*>(S + (size_t)i * D + 16 * cc)[p] =
           __fmul2_rn(T[p], make_float2(col[2 * p], col[2 * p + 1]));
   }
-  __syncthreads();
+  sync();
 }
 
 // S [D][D] in shared memory, quantized into the slot's record
 // (the quantization of sq_quantize_state). Returns status bits.
-template <int D>
-__device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8_t* dst, uint8_t* rec, const float* S) {
+template <int D, typename Sync>
+__device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8_t* dst, uint8_t* rec, const float* S,
+                                               Sync sync) {
   using G = Geo<D>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cc = lane % G::LPR, rg = warp * G::RPW + lane / G::LPR;
@@ -122,7 +125,7 @@ __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8
     phi[i] = a.t.phi[(size_t)h * D + i];
   }
   for (uint32_t x = tid * 16; x < rb; x += G::NT * 16) *reinterpret_cast<uint4*>(rec + x) = make_uint4(0, 0, 0, 0);
-  __syncthreads();  // the tables, the cleared record, and S
+  sync();  // the tables, the cleared record, and S
   const float* icol = a.t.icol + (size_t)h * D + 16 * cc;
   float2 T[G::RPT][8];
 #pragma unroll
@@ -132,7 +135,7 @@ __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8
       T[r][p] = __fmul2_rn(reinterpret_cast<const float2*>(S + (size_t)(r * G::NG + rg) * D + 16 * cc)[p],
                            make_float2(icol[2 * p], icol[2 * p + 1]));
   const uint32_t st = sqk::requant_rows<D, 0>(rec, row_off, row_code, phi, rg, cc, false, T);
-  __syncthreads();
+  sync();
   for (uint32_t x = tid * 16; x < rb; x += G::NT * 16)
     *reinterpret_cast<uint4*>(dst + x) = *reinterpret_cast<const uint4*>(rec + x);
   return st;
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   float4 S[R::RPT];
   if (n > 0) fetch(0);
   if (PACKED && resume) {
-    unpack_state<D>(a, h, record, rec, Ssh);
+    unpack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });
 #pragma unroll
     for (int r = 0; r < R::RPT; ++r) S[r] = *reinterpret_cast<const float4*>(Ssh + (row0 + r * R::RP) * D + c4);
   } else {
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   if (PACKED) {
 #pragma unroll
     for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r * R::RP) * D + c4) = S[r];
-    st |= pack_state<D>(a, h, record, rec, Ssh);  // its first barrier orders S
+    st |= pack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });  // its first barrier orders S
   } else {
 #pragma unroll
     for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(S_pool + (size_t)(row0 + r * R::RP) * D + c4) = S[r];
