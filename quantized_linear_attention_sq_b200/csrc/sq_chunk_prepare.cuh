@@ -15,10 +15,10 @@
 // keeps its precision behind a gate of zero. The inverse is formed in fp32 by
 // blocks of 16: the diagonal blocks by substitution, then pairs of blocks,
 // [T1 0; -T2 A21 T1, T2], to 32 and to 64.
-// T and P T are stored as three bf16 terms each (hi + mid + lo = the fp32
-// value to 2^-24), so that the scan's products keep fp32 accuracy; only the
-// blocks on and below the diagonal are stored, in the order the scan's matrix
-// instructions read them.
+// T and P T are stored as three bf16 terms each, whose sum is the fp32 value,
+// so that the scan's products keep fp32 accuracy; only the blocks on and
+// below the diagonal are stored, in the order the scan's matrix instructions
+// read them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,19 +27,21 @@
 
 namespace sqr {
 
-constexpr int kTerms = 3;                       // bf16 terms of an fp32 operand
-constexpr int kTriBytes = 2 * 16 * (64 + 48 + 32 + 16);       // one term of T or P T: 5120
-constexpr int kCoefFloats = 64 + 64 + 4;        // e^G, e^(G_63 - G), e^(G_63)
-constexpr int kPrepBytes = 2 * kTerms * kTriBytes + 4 * kCoefFloats;  // per block and value head
+constexpr int kTerms = 3;                                    // bf16 terms of an fp32 operand
+constexpr int kTermBytes = 32 * (128 + 96 + 64 + 32);        // one term of T and P T together
+constexpr int kCoefFloats = 64 + 64 + 4;                     // e^G, e^(G_63 - G), e^(G_63)
+constexpr int kPrepBytes = kTerms * kTermBytes + 4 * kCoefFloats;  // per block and value head
 static_assert(kPrepBytes % 16 == 0, "bulk copies move 16-byte multiples");
 
-// Byte offset of element (i, j), i >= 16 (j / 16), inside one term: column
-// block kk = j / 16 holds rows 16 kk .. 63 in groups of 8 rows x 16 columns,
-// a group as two 8 x 8 pieces of 128 contiguous bytes (the tensor core's
-// unswizzled layout).
-__host__ __device__ constexpr int tri_base(int kk) { return kk * 2048 - kk * (kk - 1) * 256; }
-__device__ __forceinline__ int tri_offset(int i, int j) {
-  const int kk = j >> 4, li = i - 16 * kk;
+// One term: for each 16 columns kk = j / 16, the operand rows that are not
+// all zero there: rows 16 kk .. 63 of T in order, then rows 63 .. 16 kk of
+// P T backwards, so that the 128 - 32 kk result columns are contiguous
+// (u_16kk .. u_63, then o_63 .. o_16kk). Rows come in groups of 8 x 16
+// columns, a group as two 8 x 8 pieces of 128 contiguous bytes (the tensor
+// core's unswizzled layout).
+__host__ __device__ constexpr int tri_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }
+__device__ __forceinline__ int tri_offset(int i, int j, bool pt) {
+  const int kk = j >> 4, li = pt ? 127 - 16 * kk - i : i - 16 * kk;
   return tri_base(kk) + (li >> 3) * 256 + ((j >> 3) & 1) * 128 + (li & 7) * 16 + (j & 7) * 2;
 }
 
@@ -65,20 +67,23 @@ __device__ __forceinline__ bool block_span(const PrepArgs& a, int c, int& first,
   return true;
 }
 
-// x = hi + mid + lo, each rounded to nearest; two values at a time.
-__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
+// x = hi + mid + lo exactly, each a bf16: an fp32 value's 24 significant bits
+// are three times 8, cut off one after the other. Two values at a time,
+// packed as (a: low half, b: high half).
+__device__ __forceinline__ uint32_t pack_high(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[kTerms]) {
-  t[0] = bf16x2(a, b);
-  a -= __uint_as_float(t[0] << 16);
-  b -= __uint_as_float(t[0] & 0xffff0000u);
-  t[1] = bf16x2(a, b);
-  a -= __uint_as_float(t[1] << 16);
-  b -= __uint_as_float(t[1] & 0xffff0000u);
-  t[2] = bf16x2(a, b);
+__device__ __forceinline__ float2 cut(float2 x) {
+  return make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+}
+__device__ __forceinline__ void split3(float2 x, uint32_t (&t)[kTerms]) {
+  const float2 hi = cut(x);
+  t[0] = pack_high(hi.x, hi.y);
+  const float2 r = __ffma2_rn(hi, make_float2(-1.0f, -1.0f), x);
+  const float2 mid = cut(r);
+  t[1] = pack_high(mid.x, mid.y);
+  const float2 lo = __ffma2_rn(mid, make_float2(-1.0f, -1.0f), r);
+  t[2] = pack_high(lo.x, lo.y);
 }
 
 constexpr int kPrepThreads = 128;
@@ -137,15 +142,15 @@ __device__ __forceinline__ void block_store(float* X, const float2 (&acc)[2][2],
 }
 __device__ __forceinline__ float* blk(float* M, int bi, int bj) { return M + 16 * bi * kPit + 16 * bj; }
 
-// Four columns of one row of block (bi, bj), times beta, as three terms.
-__device__ __forceinline__ void emit(uint8_t* out, int i, int j, float4 x, const float* beta) {
+// Four columns of a row of T or P T, times beta, as three terms.
+__device__ __forceinline__ void emit(uint8_t* out, int i, int j, bool pt, float4 x, const float* beta) {
   const float4 f = *reinterpret_cast<const float4*>(beta + j);
   uint32_t lo[kTerms], hi[kTerms];
-  split3(x.x * f.x, x.y * f.y, lo);
-  split3(x.z * f.z, x.w * f.w, hi);
-  const int at = tri_offset(i, j);
+  split3(make_float2(x.x * f.x, x.y * f.y), lo);
+  split3(make_float2(x.z * f.z, x.w * f.w), hi);
+  const int at = tri_offset(i, j, pt);
 #pragma unroll
-  for (int s = 0; s < kTerms; ++s) *reinterpret_cast<uint2*>(out + s * kTriBytes + at) = make_uint2(lo[s], hi[s]);
+  for (int s = 0; s < kTerms; ++s) *reinterpret_cast<uint2*>(out + s * kTermBytes + at) = make_uint2(lo[s], hi[s]);
 }
 
 // One CTA per block and key head; the value heads that share the key head
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_chunk_prepare(const PrepArg
   for (int hh = 0; hh < share; ++hh) {
     const int h = hk * share + hh;
     uint8_t* rec = a.ws + ((uint64_t)c * a.r.h_v + h) * kPrepBytes;
-    float* coef = reinterpret_cast<float*>(rec + 2 * kTerms * kTriBytes);
+    float* coef = reinterpret_cast<float*>(rec + kTerms * kTermBytes);
     __syncthreads();  // the dots (first head); the previous head's matrices have been read
     if (warp == 0) {
       double l[2];
@@ -285,8 +290,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_chunk_prepare(const PrepArg
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int i = 16 * pi + r0 + r, j = 16 * pj + c0;
-        emit(rec + kTerms * kTriBytes, i, j, make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y), s.beta);
-        emit(rec, i, j, *reinterpret_cast<const float4*>(T + i * kPit + j), s.beta);
+        emit(rec, i, j, true, make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y), s.beta);
+        emit(rec, i, j, false, *reinterpret_cast<const float4*>(T + i * kPit + j), s.beta);
       }
     }
   }

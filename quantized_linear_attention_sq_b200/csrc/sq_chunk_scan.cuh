@@ -8,7 +8,7 @@
 // run on the tensor cores with a transposed left operand out of tensor
 // memory, so no operand that a thread computes ever goes through shared
 // memory:
-//     D1 = S^T [k; q]^T         (A: S^T,  B: the k and q tiles as TMA left them)
+//     D1 = S^T [q; k]^T         (A: S^T,  B: the q and k tiles as TMA left them)
 //     D2 = r^T [T; P T]^T       (A: r^T,  B: the prepared block)
 //     D3 = (e^(G63 - G) u)^T k  (A: u^T,  B: the k tile again, read the other way)
 // with r = v - e^G D1k, u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
@@ -20,8 +20,10 @@
 //
 // Ten warps: eight compute (two per 32 lanes of tensor memory, sharing the
 // columns), one issues the TMA loads of the next block, one the matrix
-// products. The chain of a block is D1k -> r -> D2u -> u -> D3 -> S; the q
-// product runs under r, the P T product and o under u and D3.
+// products. The chain of a block is D1 -> r -> D2 -> u -> D3 -> S; o is
+// finished under D3 and leaves by TMA from shared memory. An instruction of
+// the tensor core costs about the same for 64 and for 128 result columns, so
+// q and k, and T and P T, share theirs.
 #pragma once
 
 #include <cuda.h>
@@ -34,17 +36,21 @@ namespace sqr {
 constexpr int kScanCompute = 256;             // threads that own a part of the state
 constexpr int kScanThreads = kScanCompute + 64;
 constexpr int kScanStages = 2;
-constexpr uint32_t kTileBytes = 64 * 128 * 2;  // q, k or v rows of a block
-constexpr uint32_t kStageBytes = 3 * kTileBytes + (kPrepBytes + 1023) / 1024 * 1024;
-constexpr uint32_t kStageTx = 3 * kTileBytes + kPrepBytes;
+constexpr uint32_t kTileBytes = 64 * 128 * 2;  // q, k, v or o rows of a block
+// A stage: channels 0..63 of the q rows, then of the k rows, the same for
+// channels 64..127 (128-byte swizzled), the v rows, the prepared block.
+constexpr uint32_t kStageV = 2 * kTileBytes, kStagePrep = 3 * kTileBytes;
+constexpr uint32_t kStageBytes = kStagePrep + (kPrepBytes + 1023) / 1024 * 1024;
+constexpr uint32_t kStageTx = kStagePrep + kPrepBytes;
+constexpr uint32_t kOutAt = kScanStages * kStageBytes;  // o rows on their way out
 
 struct ScanCtl {
   uint64_t full[kScanStages], empty[kScanStages];
-  uint64_t s_ready, r_ready, u_ready, d1, d2, d2o, d3, drain;
+  uint64_t s_ready, r_ready, u_ready, o_ready, d1, d2, d3, drain;
   uint32_t tmem;
   int32_t abort;
 };
-constexpr size_t kScanSmem = 1024 + kScanStages * kStageBytes + sizeof(ScanCtl) + 16;
+constexpr size_t kScanSmem = 1024 + kOutAt + kTileBytes + sizeof(ScanCtl) + 16;
 
 struct ScanArgs {
   PrepArgs p;
@@ -55,12 +61,11 @@ struct ScanArgs {
 constexpr uint32_t TM_S = 0;      // S^T terms: hi and mid of key rows 0..63, of 64..127, then lo; D3 takes 0..127
 constexpr uint32_t TM_U = 128;    // u^T terms (over the lo terms of S^T)
 constexpr uint32_t TM_R = 224;    // r^T terms
-constexpr uint32_t TM_D1K = 320;  // S^T k^T, then D2u
-constexpr uint32_t TM_D1Q = 384;
-constexpr uint32_t TM_D2O = 448;
+constexpr uint32_t TM_D1 = 320;   // S^T q^T, then S^T k^T
+constexpr uint32_t TM_D2 = 384;   // u^T (over S^T k^T), then the P T part of o, rows backwards
 
 // Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
-__device__ __forceinline__ uint32_t s_col(int s, int ks) {
+__host__ __device__ constexpr uint32_t s_col(int s, int ks) {
   return s == 2 ? 128u + 8u * ks : 64u * (ks >> 2) + 32u * s + 8u * (ks & 3);
 }
 
@@ -71,6 +76,16 @@ __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int 
           sqk::smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(sqk::smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(sqk::smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -103,12 +118,9 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&x)[32], uint32_t addr) {
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&x)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SQ_RW8(x, 0), SQ_RW8(x, 8), SQ_RW8(x, 16), SQ_RW8(x, 24)::"memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&x)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      SQ_W8(x, 0), SQ_W8(x, 8)
-      : "memory");
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&x)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), SQ_W8(x, 0)
+               : "memory");
 }
 
 // fp32 accumulators, bf16 operands, M = 128, N columns; `mn`: B has N contiguous.
@@ -124,16 +136,19 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 // 32 fp32 values of a lane (k index 0..31 of an A operand) to tensor memory as three terms.
 template <typename Col>
 __device__ __forceinline__ void put_terms(const float (&x)[32], uint32_t base, Col col) {
-  uint32_t t[kTerms][16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint32_t w[kTerms];
-    split3(x[2 * i], x[2 * i + 1], w);
+  for (int p = 0; p < 2; ++p) {
+    uint32_t t[kTerms][8];
 #pragma unroll
-    for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[kTerms];
+      split3(make_float2(x[16 * p + 2 * i], x[16 * p + 2 * i + 1]), w);
+#pragma unroll
+      for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
+    }
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s) tc_st8(base + col(s) + 8 * p, t[s]);
   }
-#pragma unroll
-  for (int s = 0; s < kTerms; ++s) tc_st16(base + col(s), t[s]);
 }
 
 // A warp's arrival on a barrier once its tensor memory stores are done.
@@ -157,10 +172,11 @@ __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" 
 template <bool PACKED>
 __global__ void __launch_bounds__(kScanThreads, 1)
     k_chunk_scan(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map, const ScanArgs args) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
+                 const ScanArgs args) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  ScanCtl& ctl = *reinterpret_cast<ScanCtl*>(smem + kScanStages * kStageBytes);
+  ScanCtl& ctl = *reinterpret_cast<ScanCtl*>(smem + kOutAt + kTileBytes);
   const RaggedArgs& a = args.p.r;
   const int b = blockIdx.x / a.h_v, h = blockIdx.x - b * a.h_v, hk = h / (a.h_v / a.h_k);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -188,9 +204,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     sqk::mbar_init(&ctl.s_ready, kScanCompute / 32);
     sqk::mbar_init(&ctl.r_ready, kScanCompute / 32);
     sqk::mbar_init(&ctl.u_ready, kScanCompute / 32);
+    sqk::mbar_init(&ctl.o_ready, kScanCompute / 32);
     sqk::mbar_init(&ctl.d1, 1);
     sqk::mbar_init(&ctl.d2, 1);
-    sqk::mbar_init(&ctl.d2o, 1);
     sqk::mbar_init(&ctl.d3, 1);
     sqk::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
@@ -235,13 +251,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         uint8_t* stage = smem + sg * kStageBytes;
         sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx);
         const int row = first + 64 * i;
-        tma_tile(stage + kTileBytes, &k_map, 0, hk, row, &ctl.full[sg]);
-        tma_tile(stage + kTileBytes + kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
-        tma_tile(stage + 2 * kTileBytes, &v_map, 0, h, row, &ctl.full[sg]);
-        sqk::bulk_g2s(stage + 3 * kTileBytes, args.p.ws + ((uint64_t)(c0 + i) * a.h_v + h) * kPrepBytes, kPrepBytes,
-                      &ctl.full[sg]);
         tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
-        tma_tile(stage + kTileBytes / 2, &q_map, 64, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kTileBytes / 2, &k_map, 0, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kTileBytes, &q_map, 64, hk, row, &ctl.full[sg]);
+        tma_tile(stage + 3 * kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kStageV, &v_map, 0, h, row, &ctl.full[sg]);
+        sqk::bulk_g2s(stage + kStagePrep, args.p.ws + ((uint64_t)(c0 + i) * a.h_v + h) * kPrepBytes, kPrepBytes,
+                      &ctl.full[sg]);
         issued = i + 1;
       }
       // no copy is in flight when the CTA ends
@@ -249,55 +265,55 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
     }
   } else if (warp == 9) {  // ------------------------------------- products
-    if (lane == 0) {
-      const uint32_t d64 = mma_desc(64, false), d128 = mma_desc(128, true);
-      for (int i = 0; i < blocks; ++i) {
-        const int sg = i & 1;
-        const uint32_t ph = i & 1;
-        const uint32_t stage = sqk::smem_u32(smem) + sg * kStageBytes;
-        const uint32_t qt = stage, kt = stage + kTileBytes, prep = stage + 3 * kTileBytes;
-        if (!sqk::mbar_wait_bounded(&ctl.full[sg], (i >> 1) & 1, ns) || !sqk::mbar_wait_bounded(&ctl.s_ready, ph, ns)) break;
-        tc_after();
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t tile = which ? qt : kt, d = tm + (which ? TM_D1Q : TM_D1K);
+    const uint32_t base = sqk::smem_u32(smem);
+    for (int i = 0; i < blocks; ++i) {
+      const uint32_t ph = i & 1;
+      const uint32_t stage = base + (i & 1) * kStageBytes;
+      if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns) || !warp_wait(ctl, &ctl.s_ready, ph, ns)) break;
+      tc_after();
+      if (elect_one()) {
+        const uint64_t qk = smem_desc(stage, 16, 1024, 2);
 #pragma unroll
-          for (int s = kTerms - 1; s >= 0; --s)
+        for (int s = kTerms - 1; s >= 0; --s)
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              tc_mma(d, tm + TM_S + s_col(s, ks),
-                     smem_desc(tile + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16, 1024, 2), d64,
-                     s < kTerms - 1 || ks > 0);
-          if (which == 0) tc_commit(&ctl.d1);
-        }
-        if (!sqk::mbar_wait_bounded(&ctl.r_ready, ph, ns)) break;
-        tc_after();
+          for (int ks = 0; ks < 8; ++ks)
+            tc_mma(tm + TM_D1, tm + TM_S + s_col(s, ks), qk + ((ks >> 2) * kTileBytes + (ks & 3) * 32) / 16,
+                   mma_desc(128, false), s < kTerms - 1 || ks > 0);
+        tc_commit(&ctl.d1);
+      }
+      __syncwarp();
+      if (!warp_wait(ctl, &ctl.r_ready, ph, ns)) break;
+      tc_after();
+      if (elect_one()) {
+        const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
         constexpr int pr[6] = {2, 0, 1, 1, 0, 0}, pt[6] = {0, 2, 1, 0, 1, 0};  // terms of r and of T, smallest first
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t m = prep + which * kTerms * kTriBytes, d = tm + (which ? TM_D2O : TM_D1K);
 #pragma unroll
-          for (int x = 0; x < 6; ++x)
+        for (int x = 0; x < 6; ++x)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15
-              tc_mma(d + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
-                     smem_desc(m + pt[x] * kTriBytes + tri_base(kk), 128, 256, 0), mma_desc(64 - 16 * kk, false),
-                     x > 0 || kk > 0);
-          tc_commit(which ? &ctl.d2o : &ctl.d2);
-        }
-        if (!sqk::mbar_wait_bounded(&ctl.u_ready, ph, ns)) break;
-        tc_after();
+          for (int kk = 0; kk < 4; ++kk)  // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15
+            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk, prep + (pt[x] * kTermBytes + tri_base(kk)) / 16,
+                   mma_desc(128 - 32 * kk, false), x > 0 || kk > 0);
+        tc_commit(&ctl.d2);
+      }
+      __syncwarp();
+      if (!warp_wait(ctl, &ctl.u_ready, ph, ns)) break;
+      tc_after();
+      if (elect_one()) {
+        const uint64_t kt = smem_desc(stage + kTileBytes / 2, kTileBytes, 1024, 2);
 #pragma unroll
         for (int s = kTerms - 1; s >= 0; --s)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tm + TM_S, tm + TM_U + 32 * s + 8 * ks, smem_desc(kt + ks * 2048, kTileBytes / 2, 1024, 2), d128,
+            tc_mma(tm + TM_S, tm + TM_U + 32 * s + 8 * ks, kt + ks * 2048 / 16, mma_desc(128, true),
                    s < kTerms - 1 || ks > 0);
         tc_commit(&ctl.d3);
       }
-      tc_commit(&ctl.drain);  // no product is in flight when the tensor memory is given back
-      if (!sqk::mbar_wait_bounded(&ctl.drain, 0, ns)) ctl.abort = 1;
+      __syncwarp();
     }
+    // no product is in flight when the tensor memory is given back
+    if (elect_one()) tc_commit(&ctl.drain);
+    __syncwarp();
+    warp_wait(ctl, &ctl.drain, 0, ns);
   } else {  // -------------------------------------------------- the rest
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     auto put_state = [&]() {
@@ -316,12 +332,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (live < 64) {
         // rows of the k tile behind the request's last: another request's, or none's
         for (int x = tid; x < (64 - live) * 16; x += kScanCompute)
-          *reinterpret_cast<uint4*>(stage + kTileBytes + ((x >> 3) & 1) * (kTileBytes / 2) + (live + (x >> 4)) * 128 +
+          *reinterpret_cast<uint4*>(stage + kTileBytes / 2 + ((x >> 3) & 1) * kTileBytes + (live + (x >> 4)) * 128 +
                                     (x & 7) * 16) = make_uint4(0, 0, 0, 0);
         sqk::fence_proxy_async_smem();
       }
-      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + 2 * kTileBytes) + 32 * half * 128 + col;
-      const float* coef = reinterpret_cast<const float*>(stage + 3 * kTileBytes + 2 * kTerms * kTriBytes);
+      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 32 * half * 128 + col;
+      const float* coef = reinterpret_cast<const float*>(stage + kStagePrep + kTerms * kTermBytes);
       const float4* eg = reinterpret_cast<const float4*>(coef + 32 * half);
       const float4* ed = reinterpret_cast<const float4*>(coef + 64 + 32 * half);
       const int mine = live - 32 * half;  // live rows of this half
@@ -331,7 +347,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       for (int j = 0; j < 32; ++j) x[j] = j < mine ? __bfloat162float(v[j * 128]) : 0.0f;
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
-      tc_ld32(w, tl + TM_D1K + 32 * half);
+      tc_ld32(w, tl + TM_D1 + 64 + 32 * half);
       tc_wait_ld(w);
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
@@ -341,12 +357,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
         x[j + 3] = j + 3 < mine ? fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]) : 0.0f;
       }
+      // the block before's o has left its staging rows: this warp's arrival leads to the next D2, before which no
+      // other warp writes there
+      if (tid == 0) sqk::bulk_wait_read_all();
+      __syncwarp();
       put_terms(x, tl + TM_R + 16 * half, [](int s) { return 32u * s; });
       warp_arrive(&ctl.r_ready);
 
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
       tc_after();
-      tc_ld32(w, tl + TM_D1K + 32 * half);
+      tc_ld32(w, tl + TM_D2 + 32 * half);
       tc_wait_ld(w);
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
@@ -360,48 +380,60 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       warp_arrive(&ctl.u_ready);
 
       // o, under the state's product
-      if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
-      tc_after();
       {
         uint32_t y[32];
-        tc_ld32(w, tl + TM_D1Q + 32 * half);
-        tc_ld32(y, tl + TM_D2O + 32 * half);
+        tc_ld32(w, tl + TM_D1 + 32 * half);
+        tc_ld32(y, tl + TM_D2 + 96 - 32 * half);
         tc_wait_ld(w);
         tc_wait_ld(y);
-        __nv_bfloat16* op = out + ((size_t)(first + 64 * i + 32 * half) * a.h_v + h) * 128 + col;
+        __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(smem + kOutAt) + 32 * half * 128 + col;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 e4 = eg[j >> 2];
           const float e[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float o = fmaf(e[k], __uint_as_float(w[j + k]), __uint_as_float(y[j + k]));
-            if (j + k < mine) {
-              if (o != o) st |= ST_NAN;
-              op[(size_t)(j + k) * a.h_v * 128] = __float2bfloat16_rn(o);
-            }
+            const float o = fmaf(e[k], __uint_as_float(w[j + k]), __uint_as_float(y[31 - j - k]));
+            if (o != o && j + k < mine) st |= ST_NAN;
+            op[(j + k) * 128] = __float2bfloat16_rn(o);
           }
+        }
+      }
+      sqk::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
+      if (live < 64) {  // the last block: its live rows only
+        if (!warp_wait(ctl, &ctl.o_ready, ph, ns)) break;
+        for (int y = tid; y < live * 16; y += kScanCompute)
+          reinterpret_cast<uint4*>(out + ((size_t)(first + 64 * i + (y >> 4)) * a.h_v + h) * 128)[y & 15] =
+              reinterpret_cast<const uint4*>(smem + kOutAt)[y];
+      } else if (warp == 0) {
+        if (!warp_wait(ctl, &ctl.o_ready, ph, ns)) break;
+        if (lane == 0) {
+          tma_store(&o_map, 0, h, first + 64 * i, smem + kOutAt);
+          sqk::bulk_commit();
         }
       }
       const float g63 = coef[128];
       if (!warp_wait(ctl, &ctl.d3, ph, ns)) break;
       tc_after();
-      {
-        uint32_t y[32];
-        tc_ld32(w, tl + TM_S + 64 * half);
-        tc_ld32(y, tl + TM_S + 64 * half + 32);
-        tc_wait_ld(w);
-        tc_wait_ld(y);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          S[0][j] = fmaf(g63, S[0][j], __uint_as_float(w[j]));
-          S[1][j] = fmaf(g63, S[1][j], __uint_as_float(y[j]));
+      for (int y = 0; y < 2; ++y) {
+        tc_ld32(w, tl + TM_S + 64 * half + 32 * y);
+        tc_wait_ld(w);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float2 t = __ffma2_rn(make_float2(g63, g63), make_float2(S[y][j], S[y][j + 1]),
+                                      make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])));
+          S[y][j] = t.x;
+          S[y][j + 1] = t.y;
         }
       }
       if (lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before the loads above
       if (i + 1 < blocks) put_state();
     }
   }
+  if (tid == 0) sqk::bulk_wait_all();
   tc_before();
   __syncthreads();
   tc_after();

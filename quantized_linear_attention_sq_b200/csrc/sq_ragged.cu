@@ -133,10 +133,11 @@ sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_r
   a.p.ws = static_cast<uint8_t*>(workspace);
   a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
   a.wait_ns = h->wait_ns;
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm, om;
   sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (s == SQ_OK) s = row_map(&om, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (s != SQ_OK) return s;
   cudaError_t e = cudaFuncSetAttribute(sqr::k_chunk_prepare, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(sqr::PrepSmem));
@@ -147,7 +148,7 @@ sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_r
   sqr::k_chunk_prepare<<<(unsigned)a.p.n_blocks * r.h_k, sqr::kPrepThreads, sizeof(sqr::PrepSmem), st>>>(a.p);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
-    scan<<<r.B * r.h_v, sqr::kScanThreads, sqr::kScanSmem, st>>>(qm, km, vm, a);
+    scan<<<r.B * r.h_v, sqr::kScanThreads, sqr::kScanSmem, st>>>(qm, km, vm, om, a);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? SQ_OK : cuda_fail(e, "launching the block kernels");
