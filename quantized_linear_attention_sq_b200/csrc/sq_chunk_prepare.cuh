@@ -4,21 +4,26 @@
 // With G_i the sum of log gates of the block's rows 0..i, S the state before
 // the block, and for i > j (i >= j for P)
 //     A_ij = beta_i e^(G_i - G_j) k_i . k_j,   P_ij = e^(G_i - G_j) q_i . k_j,
-// the rows' updates u solve (1 + A) u = beta (v - e^G (k S)), so with
-// T = (1 + A)^-1 diag(beta)
-//     u = T r,   r_j = v_j - e^(G_j) k_j S,   o = e^G q S + (P T) r,
+// the rows' updates u solve (1 + A) u = r, so with T = (1 + A)^-1
+//     u = T r,   r_j = beta_j (v_j - e^(G_j) k_j S),   o = e^G q S + (P T) r,
 //     S <- e^(G_63) S + sum_i e^(G_63 - G_i) k_i u_i^T.
 // This kernel forms T and P T of every block and value head, in parallel over
 // blocks, for sq_chunk_scan.cuh, which walks a request's blocks in order.
 // q, k are bf16: their products are exact, accumulated in fp32 by the tensor
-// cores. Gates are accumulated as fp64 logarithms: a difference G_i - G_j
-// keeps its precision behind a gate of zero. The inverse is formed in fp32 by
-// blocks of 16: the diagonal blocks by substitution, then pairs of blocks,
-// [T1 0; -T2 A21 T1, T2], to 32 and to 64.
-// T and P T are stored as three bf16 terms each, whose sum is the fp32 value,
-// so that the scan's products keep fp32 accuracy; only the blocks on and
-// below the diagonal are stored, in the order the scan's matrix instructions
-// read them.
+// cores, and stay in registers for the value heads that share them. Logs of
+// gates are summed as pairs of fp32: a difference G_i - G_j keeps its
+// precision behind a gate of zero. Decays are products of factors that are
+// all at most one (token to the end of its 16, from the start of its 16,
+// between 16s; formed pair by pair inside a 16), so a block needs a fourth of
+// the exponentials. The inverse goes by blocks of 16: those on the diagonal
+// by substitution in fp32, then pairs of blocks, [T1 0; -T2 A21 T1, T2], to
+// 32 and to 64 on the tensor cores, every operand as three bf16 terms whose
+// sum is the fp32 value (the six largest of nine products: fp32 accuracy).
+// T leaves as those terms; P T only reaches o, a bf16 result, and is formed
+// from and stored as two (2^-16). Only the blocks on and below the diagonal
+// are stored, in the order the scan's matrix instructions read them.
+// Bound by latency: a value head is a chain of six short phases with a
+// barrier between them, and four CTAs per SM run theirs against each other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,22 +32,25 @@
 
 namespace sqr {
 
-constexpr int kTerms = 3;                                    // bf16 terms of an fp32 operand
-constexpr int kTermBytes = 32 * (128 + 96 + 64 + 32);        // one term of T and P T together
-constexpr int kCoefFloats = 64 + 64 + 4;                     // e^G, e^(G_63 - G), e^(G_63)
-constexpr int kPrepBytes = kTerms * kTermBytes + 4 * kCoefFloats;  // per block and value head
+constexpr int kTerms = 3;                                    // bf16 terms of an fp32 operand of the state's path
+constexpr int kOutTerms = 2;                                 // terms of P T
+constexpr int kTriBytes = 32 * (64 + 48 + 32 + 16);          // one term of one matrix
+constexpr int kTermsBytes = (kTerms + kOutTerms) * kTriBytes;
+constexpr int kCoefFloats = 4 * 64 + 4;                      // e^G, beta, beta e^G, e^(G_63 - G), e^(G_63)
+constexpr int kPrepBytes = kTermsBytes + 4 * kCoefFloats;    // per block and value head
 static_assert(kPrepBytes % 16 == 0, "bulk copies move 16-byte multiples");
 
-// One term: for each 16 columns kk = j / 16, the operand rows that are not
-// all zero there: rows 16 kk .. 63 of T in order, then rows 63 .. 16 kk of
-// P T backwards, so that the 128 - 32 kk result columns are contiguous
-// (u_16kk .. u_63, then o_63 .. o_16kk). Rows come in groups of 8 x 16
-// columns, a group as two 8 x 8 pieces of 128 contiguous bytes (the tensor
-// core's unswizzled layout).
-__host__ __device__ constexpr int tri_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }
-__device__ __forceinline__ int tri_offset(int i, int j, bool pt) {
-  const int kk = j >> 4, li = pt ? 127 - 16 * kk - i : i - 16 * kk;
-  return tri_base(kk) + (li >> 3) * 256 + ((j >> 3) & 1) * 128 + (li & 7) * 16 + (j & 7) * 2;
+// Terms 0 and 1 hold T and P T together: for each 16 columns kk = j / 16, the
+// operand rows that are not all zero there, rows 16 kk .. 63 of T in order,
+// then rows 63 .. 16 kk of P T backwards, so that the 128 - 32 kk result
+// columns are contiguous (u_16kk .. u_63, then o_63 .. o_16kk). Term 2 is T
+// alone. Rows come in groups of 8 x 16 columns, a group as two 8 x 8 pieces
+// of 128 contiguous bytes (the tensor core's unswizzled layout).
+__host__ __device__ constexpr int term_base(int s) { return s * 2 * kTriBytes; }
+__host__ __device__ constexpr int pair_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }  // within terms 0, 1
+__host__ __device__ constexpr int tri_base(int kk) { return pair_base(kk) / 2; }                 // within term 2
+__device__ __forceinline__ int row_piece(int li, int j) {
+  return (li >> 3) * 256 + ((j >> 3) & 1) * 128 + (li & 7) * 16 + (j & 7) * 2;
 }
 
 struct PrepArgs {
@@ -85,25 +93,56 @@ __device__ __forceinline__ void split3(float2 x, uint32_t (&t)[kTerms]) {
   const float2 lo = __ffma2_rn(mid, make_float2(-1.0f, -1.0f), r);
   t[2] = pack_high(lo.x, lo.y);
 }
+// The first two terms only, the second rounded to nearest.
+__device__ __forceinline__ void split2(float2 x, uint32_t* t) {
+  const float2 hi = cut(x);
+  t[0] = pack_high(hi.x, hi.y);
+  const float2 r = __ffma2_rn(hi, make_float2(-1.0f, -1.0f), x);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(t[1]) : "f"(r.y), "f"(r.x));
+}
 
 constexpr int kPrepThreads = 128;
 constexpr int kTile = 136;   // bf16 per row of the q and k tiles (16 bytes of padding)
-constexpr int kPit = 68;     // floats per row of the 64 x 64 matrices
+constexpr int kBlk = 512;    // bytes of one 16 x 16 bf16 block
+
+// 16 bytes (columns 8 half .. + 7) of row r of such a block: swapped in every
+// other four rows, so that the eight rows of a matrix load lie in different banks.
+__device__ __forceinline__ int blk_piece(int r, int half) { return r * 32 + ((half ^ ((r >> 2) & 1)) << 4); }
+
+// Factors of the rows of one value head; R_b is G at the end of 16 number b.
+struct PrepGate {
+  float2 G[64];      // log2, high and low part
+  float beta[64];
+  float from[64];    // e^(G_i - R_(b-1))  from its 16's start
+  float to[64];      // e^(R_b - G_j)      to its 16's end
+  float hop[4][4];   // e^(R_(bi-1) - R_bj), bj < bi
+  float diag[4][16][20];  // e^(G_i - G_j) inside the 16s, 0 above the diagonal
+};
 struct PrepSmem {
   union {
     __nv_bfloat16 qk[2][64 * kTile];
-    float m[2][64 * kPit];   // A (later P), T
+    struct {
+      uint8_t A[6][kTerms][kBlk];       // blocks below the diagonal
+      uint8_t P[10][kOutTerms][kBlk];   // blocks on and below it
+      float Ad[4][16][20];              // A's blocks on it
+    } m;
   };
-  float kk[64 * kPit], qk_dot[64 * kPit];
-  double G[64];
-  float beta[64];
+  uint8_t T[10][kTerms][kBlk];
+  PrepGate gate[2];  // two value heads at a time
+  float2 part[4];    // log gates summed by each warp
 };
-static_assert(sizeof(__nv_bfloat16) * 2 * 64 * kTile == sizeof(float) * 2 * 64 * kPit, "same size");
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(sqk::smem_u32(p)));
+               : "r"(sqk::smem_u32(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(sqk::smem_u32(p))
+               : "memory");
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -112,56 +151,121 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// acc += X Y for 16 x 16 blocks (rows kPit floats apart), one warp: lane owns
-// rows 2 (lane / 4), + 1 and columns 4 (lane % 4) .. + 3.
-__device__ __forceinline__ void block_product(float2 (&acc)[2][2], const float* X, const float* Y) {
-  const int lane = threadIdx.x & 31;
-  const float* x0 = X + 2 * (lane >> 2) * kPit;
-  const float* y0 = Y + 4 * (lane & 3);
+// A 16 x 16 fp32 block in the instruction's result layout: lane owns rows
+// lane / 4 (elements 0, 1) and + 8 (2, 3), columns 8 x + 2 (lane % 4), + 1.
+struct Acc {
+  float c[2][4];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int l = 0; l < 16; l += 4) {
-    const float4 a = *reinterpret_cast<const float4*>(x0 + l), b = *reinterpret_cast<const float4*>(x0 + kPit + l);
-    const float xa[4] = {a.x, a.y, a.z, a.w}, xb[4] = {b.x, b.y, b.z, b.w};
+    for (int y = 0; y < 4; ++y) c[0][y] = c[1][y] = 0.0f;
+  }
+  __device__ __forceinline__ void add(const uint32_t (&a)[4], const uint32_t (&b)[4]) {  // += A B, b read transposed
+    mma_bf16(c[0], a, b[0], b[1]);
+    mma_bf16(c[1], a, b[2], b[3]);
+  }
+};
+using Terms = uint32_t[kTerms][4];
+__device__ __forceinline__ void add6(Acc& acc, const Terms& a, const Terms& b) {  // smallest products first
+  acc.add(a[2], b[0]);
+  acc.add(a[0], b[2]);
+  acc.add(a[1], b[1]);
+  acc.add(a[1], b[0]);
+  acc.add(a[0], b[1]);
+  acc.add(a[0], b[0]);
+}
+// The result layout is the left operand's.
+__device__ __forceinline__ void acc_terms(const Acc& acc, Terms& t) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const float4 y = *reinterpret_cast<const float4*>(y0 + (l + m) * kPit);
-      const float2 ylo = make_float2(y.x, y.y), yhi = make_float2(y.z, y.w);
-      acc[0][0] = __ffma2_rn(make_float2(xa[m], xa[m]), ylo, acc[0][0]);
-      acc[0][1] = __ffma2_rn(make_float2(xa[m], xa[m]), yhi, acc[0][1]);
-      acc[1][0] = __ffma2_rn(make_float2(xb[m], xb[m]), ylo, acc[1][0]);
-      acc[1][1] = __ffma2_rn(make_float2(xb[m], xb[m]), yhi, acc[1][1]);
-    }
+  for (int x = 0; x < 4; ++x) {
+    uint32_t w[kTerms];
+    split3(make_float2(acc.c[x >> 1][2 * (x & 1)], acc.c[x >> 1][2 * (x & 1) + 1]), w);
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s) t[s][x] = w[s];
   }
 }
-__device__ __forceinline__ void block_store(float* X, const float2 (&acc)[2][2], float f) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void put_left(uint8_t* block, const uint32_t (&t)[4]) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, at = 4 * (lane & 3);
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-    *reinterpret_cast<float4*>(X + (2 * (lane >> 2) + r) * kPit + 4 * (lane & 3)) =
-        make_float4(f * acc[r][0].x, f * acc[r][0].y, f * acc[r][1].x, f * acc[r][1].y);
+  for (int x = 0; x < 4; ++x)
+    *reinterpret_cast<uint32_t*>(block + blk_piece(r + 8 * (x & 1), x >> 1) + at) = t[x];
 }
-__device__ __forceinline__ float* blk(float* M, int bi, int bj) { return M + 16 * bi * kPit + 16 * bj; }
 
-// Four columns of a row of T or P T, times beta, as three terms.
-__device__ __forceinline__ void emit(uint8_t* out, int i, int j, bool pt, float4 x, const float* beta) {
-  const float4 f = *reinterpret_cast<const float4*>(beta + j);
-  uint32_t lo[kTerms], hi[kTerms];
-  split3(make_float2(x.x * f.x, x.y * f.y), lo);
-  split3(make_float2(x.z * f.z, x.w * f.w), hi);
-  const int at = tri_offset(i, j, pt);
+// Row, column and number of the blocks on and below the diagonal.
+__device__ __forceinline__ int tri_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
+__device__ __forceinline__ int tri_col(int t) { return t - tri_row(t) * (tri_row(t) + 1) / 2; }
+__device__ __forceinline__ int tri(int bi, int bj) { return bi * (bi + 1) / 2 + bj; }
+__device__ __forceinline__ int below(int bi, int bj) { return bi * (bi - 1) / 2 + bj; }
+
+// 2^x to 2 ulp, 0 for results below 2^-126.
+__device__ __forceinline__ float pow2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// a + b as an unevaluated pair (the rounding error of the high parts is kept).
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
+  return make_float2(s, __fadd_rn(e, __fadd_rn(a.y, b.y)));
+}
+__device__ __forceinline__ float pair_diff(float2 a, float2 b) {
+  return __fadd_rn(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y));
+}
+
+// Gates, betas and decay factors of value heads h and h + 1 (`heads` of
+// them), a thread for each row of each; `rec`: their records, whose factors
+// are written here.
+__device__ __forceinline__ void prepare_gates(const PrepArgs& a, PrepSmem& sm, uint8_t* rec, int first, int n, int h,
+                                              int heads) {
+  const int tid = threadIdx.x, lane = tid & 31, which = tid >> 6, i = tid & 63;
+  const bool on = which < heads;
+  PrepGate& s = sm.gate[which];
+  const size_t at = (size_t)(first + min(i, n - 1)) * a.r.h_v + h + (on ? which : 0);
+  const float g = i < n ? clamp_gate(a.r.g[at]) : 1.0f;
+  const float beta = i < n ? a.r.beta[at] : 0.0f;
+  // a gate of zero counts as 2^-126; a NaN stays one. log2f is good to an
+  // ulp: over decays that matter the sum of those errors is below 2^-22.
+  float2 G = make_float2(log2f(g < 1.17549435e-38f ? 1.17549435e-38f : g), 0.0f);
 #pragma unroll
-  for (int s = 0; s < kTerms; ++s) *reinterpret_cast<uint2*>(out + s * kTermBytes + at) = make_uint2(lo[s], hi[s]);
+  for (int d = 1; d < 32; d <<= 1) {
+    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, G.x, d), __shfl_up_sync(0xffffffffu, G.y, d));
+    if (lane >= d) G = pair_add(G, y);
+  }
+  if (lane == 31) sm.part[tid >> 5] = G;
+  __syncthreads();
+  if (i >= 32) G = pair_add(G, sm.part[2 * which]);
+  s.G[i] = G;
+  __syncthreads();
+  const float2 zero = make_float2(0.0f, 0.0f), end = s.G[63], mine = s.G[i | 15], prev = i < 16 ? zero : s.G[(i & ~15) - 1];
+  s.beta[i] = beta;
+  s.from[i] = pow2(pair_diff(G, prev));
+  s.to[i] = pow2(pair_diff(mine, G));
+  const float2* G16 = s.G + (i & ~15);
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) s.diag[i >> 4][i & 15][j] = j <= (i & 15) ? pow2(pair_diff(G, G16[j])) : 0.0f;
+  const int bi = (i >> 2) & 3, bj = i & 3;
+  if (i < 16 && bj < bi) s.hop[bi][bj] = pow2(pair_diff(s.G[16 * bi - 1], s.G[16 * bj + 15]));
+  if (on) {
+    float* coef = reinterpret_cast<float*>(rec + (size_t)which * kPrepBytes + kTermsBytes);
+    const float e = pow2(pair_diff(G, zero));
+    coef[i] = e;
+    coef[64 + i] = beta;
+    coef[128 + i] = beta * e;
+    coef[192 + i] = pow2(pair_diff(end, G));
+    if (i < 4) coef[256 + i] = pow2(pair_diff(end, zero));
+  }
 }
 
 // One CTA per block and key head; the value heads that share the key head
 // share q . k and k . k.
-__global__ void __launch_bounds__(kPrepThreads, 3) k_chunk_prepare(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int c = blockIdx.x / a.r.h_k, hk = blockIdx.x - c * a.r.h_k;
   int first, n;
   if (!block_span(a, c, first, n)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#pragma unroll 8
   for (int x = tid; x < 2 * 64 * 16; x += kPrepThreads) {
     const int which = x >> 10, row = (x >> 4) & 63, piece = x & 15;
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(which ? a.r.k : a.r.q) +
@@ -171,12 +275,13 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_chunk_prepare(const PrepArg
     *reinterpret_cast<uint4*>(&s.qk[which][row * kTile + 8 * piece]) = v;
   }
   __syncthreads();
-  // the ten 16 x 16 blocks on and below the diagonal of k k^T and of q k^T
-  for (int item = warp; item < 20; item += 4) {
-    const int t = item >> 1, which = item & 1;  // 0: q k^T, 1: k k^T
-    const int bi = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
-    const int bj = t - bi * (bi + 1) / 2;
-    float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+  // the ten blocks on and below the diagonal of q k^T (even items) and of
+  // k k^T (odd ones), five for each warp
+  Acc dot[5];
+#pragma unroll
+  for (int x = 0; x < 5; ++x) {
+    const int item = warp + 4 * x, which = item & 1, bi = tri_row(item >> 1), bj = tri_col(item >> 1);
+    dot[x].zero();
     const __nv_bfloat16* A = &s.qk[which][(16 * bi + (lane & 15)) * kTile + 8 * (lane >> 4)];
     const __nv_bfloat16* Bm = &s.qk[1][(16 * bj + (lane & 7) + 8 * (lane >> 4)) * kTile + 8 * ((lane >> 3) & 1)];
 #pragma unroll
@@ -184,114 +289,153 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_chunk_prepare(const PrepArg
       uint32_t fa[4], fb[4];
       ldmatrix4(fa, A + 16 * ks);
       ldmatrix4(fb, Bm + 16 * ks);
-      mma_bf16(c0, fa, fb[0], fb[1]);
-      mma_bf16(c1, fa, fb[2], fb[3]);
+      dot[x].add(fa, fb);
     }
-    float* D = blk(which ? s.kk : s.qk_dot, bi, bj) + (lane >> 2) * kPit + 2 * (lane & 3);
-    *reinterpret_cast<float2*>(D) = make_float2(c0[0], c0[1]);
-    *reinterpret_cast<float2*>(D + 8) = make_float2(c1[0], c1[1]);
-    *reinterpret_cast<float2*>(D + 8 * kPit) = make_float2(c0[2], c0[3]);
-    *reinterpret_cast<float2*>(D + 8 * kPit + 8) = make_float2(c1[2], c1[3]);
   }
-  float *A = s.m[0], *T = s.m[1];
   const int share = a.r.h_v / a.r.h_k;
+  const int j2 = 2 * (lane & 3), r4 = lane >> 2;
+  const int piece = blk_piece(lane & 15, lane >> 4);  // this lane's row of a matrix load
+#pragma unroll 1
   for (int hh = 0; hh < share; ++hh) {
     const int h = hk * share + hh;
     uint8_t* rec = a.ws + ((uint64_t)c * a.r.h_v + h) * kPrepBytes;
-    float* coef = reinterpret_cast<float*>(rec + kTerms * kTermBytes);
-    __syncthreads();  // the dots (first head); the previous head's matrices have been read
-    if (warp == 0) {
-      double l[2];
+    if ((hh & 1) == 0) prepare_gates(a, s, rec, first, n, h, min(2, share - hh));
+    const PrepGate& gt = s.gate[hh & 1];
+    __syncthreads();  // the factors; the tiles (first head) or the previous head's matrices have been read
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * lane + x;
-        const size_t at = (size_t)(first + min(i, n - 1)) * a.r.h_v + h;
-        const float g = i < n ? clamp_gate(a.r.g[at]) : 1.0f;
-        s.beta[i] = i < n ? a.r.beta[at] : 0.0f;
-        // a gate of zero counts as 2^-126; a NaN stays one
-        l[x] = log2((double)(g < 1.17549435e-38f ? 1.17549435e-38f : g));
-      }
-      double sum = l[0] + l[1], inc = sum;
+    for (int x = 0; x < 5; ++x) {
+      const int item = warp + 4 * x, which = item & 1, bi = tri_row(item >> 1), bj = tri_col(item >> 1);
+      Acc m;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
+      for (int y = 0; y < 2; ++y) {
+        const int i = 16 * bi + r4 + 8 * y;
+        float f = which ? gt.beta[i] : 1.0f;
+        const float* col;
+        if (bi == bj) {
+          col = gt.diag[bi][r4 + 8 * y];
+        } else {
+          col = gt.to + 16 * bj;
+          f *= gt.from[i] * gt.hop[bi][bj];
+        }
+        const float2 t0 = *reinterpret_cast<const float2*>(col + j2);
+        const float2 t1 = *reinterpret_cast<const float2*>(col + j2 + 8);
+        m.c[0][2 * y] = f * t0.x * dot[x].c[0][2 * y];
+        m.c[0][2 * y + 1] = f * t0.y * dot[x].c[0][2 * y + 1];
+        m.c[1][2 * y] = f * t1.x * dot[x].c[1][2 * y];
+        m.c[1][2 * y + 1] = f * t1.y * dot[x].c[1][2 * y + 1];
       }
-      const double G0 = inc - l[1], G1 = inc, G63 = __shfl_sync(0xffffffffu, inc, 31);
-      s.G[2 * lane] = G0;
-      s.G[2 * lane + 1] = G1;
-      reinterpret_cast<float2*>(coef)[lane] = make_float2(exp2f((float)G0), exp2f((float)G1));
-      reinterpret_cast<float2*>(coef + 64)[lane] = make_float2(exp2f((float)(G63 - G0)), exp2f((float)(G63 - G1)));
-      if (lane < 4) coef[128 + lane] = exp2f((float)G63);
+      if (which && bi == bj) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            *reinterpret_cast<float2*>(&s.m.Ad[bi][r4 + 8 * y][j2 + 8 * z]) = make_float2(m.c[z][2 * y], m.c[z][2 * y + 1]);
+      } else {
+        Terms t;
+        acc_terms(m, t);
+        uint8_t* dst = which ? s.m.A[below(bi, bj)][0] : s.m.P[tri(bi, bj)][0];
+        put_left(dst, t[0]);
+        put_left(dst + kBlk, t[1]);
+        if (which) put_left(dst + 2 * kBlk, t[2]);
+      }
     }
     __syncthreads();
-    for (int x = tid; x < 10 * 256; x += kPrepThreads) {
-      const int t = x >> 8, bi = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, bj = t - bi * (bi + 1) / 2;
-      const int i = 16 * bi + ((x >> 4) & 15), j = 16 * bj + (x & 15);
-      A[i * kPit + j] = i > j ? s.beta[i] * (exp2f((float)(s.G[i] - s.G[j])) * s.kk[i * kPit + j]) : 0.0f;
-    }
-    __syncthreads();
-    {  // diagonal blocks: lane owns a column of its warp's block (both half warps the same)
-      const float* Ad = blk(A, warp, warp);
-      float* Td = blk(T, warp, warp);
-      const int col = lane & 15;
+    {  // the block on the diagonal: lane owns a column of its warp's (both half warps the same)
+      const float (*Ad)[20] = s.m.Ad[warp];
+      const int col = lane & 15, half = lane >> 4;
       float t[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float acc = i == col ? 1.0f : 0.0f;
 #pragma unroll
-        for (int l = 0; l < i; ++l) acc = fmaf(-Ad[i * kPit + l], t[l], acc);
+        for (int l = 0; l < i; ++l) acc = fmaf(-Ad[i][l], t[l], acc);
         t[i] = acc;
       }
-      if (lane < 16) {
+      uint8_t* dst = s.T[tri(warp, warp)][0] + 2 * (col & 7);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) Td[i * kPit + col] = t[i];
+      for (int i = 0; i < 8; ++i) {  // each half warp stores eight rows
+        float v = half ? t[8 + i] : t[i];
+        uint8_t* p = dst + blk_piece(8 * half + i, col >> 3);
+#pragma unroll
+        for (int u = 0; u < kTerms; ++u) {
+          const uint32_t w = __float_as_uint(v);
+          *reinterpret_cast<uint16_t*>(p + u * kBlk) = (uint16_t)(w >> 16);
+          v -= __uint_as_float(w & 0xffff0000u);
+        }
       }
     }
-    // pairs of blocks to 32 and pairs of those to 64; intermediate products go
-    // to the unused blocks above the diagonal
-    auto zero = [](float2 (&x)[2][2]) { x[0][0] = x[0][1] = x[1][0] = x[1][1] = make_float2(0.f, 0.f); };
-    float2 acc[2][2];
-    __syncthreads();
-    if (warp < 2) {
-      const int p = 2 * warp;
-      zero(acc);
-      block_product(acc, blk(A, p + 1, p), blk(T, p, p));
-      block_store(blk(T, p, p + 1), acc, 1.0f);
-      __syncwarp();
-      zero(acc);
-      block_product(acc, blk(T, p + 1, p + 1), blk(T, p, p + 1));
-      block_store(blk(T, p + 1, p), acc, -1.0f);
-    }
-    __syncthreads();
-    const int bi = warp >> 1, bj = warp & 1;
-    zero(acc);
-    for (int l = bj; l < 2; ++l) block_product(acc, blk(A, 2 + bi, l), blk(T, l, bj));
-    block_store(blk(T, bi, 2 + bj), acc, 1.0f);
-    __syncthreads();
-    zero(acc);
-    for (int l = 0; l <= bi; ++l) block_product(acc, blk(T, 2 + bi, 2 + l), blk(T, l, 2 + bj));
-    block_store(blk(T, 2 + bi, bj), acc, -1.0f);
-    // A has been used: P takes its place
-    for (int x = tid; x < 10 * 256; x += kPrepThreads) {
-      const int t = x >> 8, pi = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, pj = t - pi * (pi + 1) / 2;
-      const int i = 16 * pi + ((x >> 4) & 15), j = 16 * pj + (x & 15);
-      A[i * kPit + j] = i >= j ? exp2f((float)(s.G[i] - s.G[j])) * s.qk_dot[i * kPit + j] : 0.0f;
-    }
-    __syncthreads();
-    // P T: five block products for each warp; T and P T leave as three terms
-    const int r0 = 2 * (lane >> 2), c0 = 4 * (lane & 3);
-    const int todo[4] = {0x3000, 0x2010, 0x3121, 0x32112233};  // (bi, bj) of each warp, low digits first
-    const int count[4] = {2, 2, 2, 4};
-    for (int x = 0; x < count[warp]; ++x) {
-      const int code = (todo[warp] >> (8 * x)) & 0xff, pi = code >> 4, pj = code & 15;
-      zero(acc);
-      for (int l = pj; l <= pi; ++l) block_product(acc, blk(A, pi, l), blk(T, l, pj));
+    // the other blocks, T(R, C) = -sum_l (sum_m T(R, m) A(m, l)) T(l, C): of
+    // the pairs of blocks (stage 0: two warps), then of the pairs of those
+#pragma unroll 1
+    for (int stage = 0; stage < 2; ++stage) {
+      __syncthreads();
+      if (stage == 0 && warp >= 2) continue;
+      const int R = stage ? 2 + (warp >> 1) : 2 * warp + 1, C = stage ? warp & 1 : 2 * warp;
+      const int m0 = stage ? 2 : R, l1 = stage ? 1 : C;
+      Acc acc, y;
+      Terms ta, tb;
+      acc.zero();
+#pragma unroll 1
+      for (int l = C; l <= l1; ++l) {
+        y.zero();
+#pragma unroll 1
+        for (int m = m0; m <= R; ++m) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int i = 16 * pi + r0 + r, j = 16 * pj + c0;
-        emit(rec, i, j, true, make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y), s.beta);
-        emit(rec, i, j, false, *reinterpret_cast<const float4*>(T + i * kPit + j), s.beta);
+          for (int u = 0; u < kTerms; ++u) {
+            ldmatrix4(ta[u], s.T[tri(R, m)][u] + piece);
+            ldmatrix4t(tb[u], s.m.A[below(m, l)][u] + piece);
+          }
+          add6(y, ta, tb);
+        }
+        acc_terms(y, ta);
+#pragma unroll
+        for (int u = 0; u < kTerms; ++u) ldmatrix4t(tb[u], s.T[tri(l, C)][u] + piece);
+        add6(acc, ta, tb);
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        acc.c[0][z] = -acc.c[0][z];
+        acc.c[1][z] = -acc.c[1][z];
+      }
+      acc_terms(acc, ta);
+#pragma unroll
+      for (int u = 0; u < kTerms; ++u) put_left(s.T[tri(R, C)][u], ta[u]);
+    }
+    __syncthreads();
+    // P T: five block products for each warp; T and P T leave
+    const uint32_t todo = warp == 0 ? 0x3000u : warp == 1 ? 0x2010u : warp == 2 ? 0x3121u : 0x32112233u;  // (bi, bj)
+    const int count = warp < 3 ? 2 : 4;
+#pragma unroll 1
+    for (int x = 0; x < count; ++x) {
+      const int pi = (todo >> (8 * x + 4)) & 15, pj = (todo >> (8 * x)) & 15;
+      Acc acc;
+      acc.zero();
+#pragma unroll 1
+      for (int l = pj; l <= pi; ++l) {
+        uint32_t pa[kOutTerms][4], tb[kOutTerms][4];
+#pragma unroll
+        for (int u = 0; u < kOutTerms; ++u) {
+          ldmatrix4(pa[u], s.m.P[tri(pi, l)][u] + piece);
+          ldmatrix4t(tb[u], s.T[tri(l, pj)][u] + piece);
+        }
+        acc.add(pa[1], tb[0]);
+        acc.add(pa[0], tb[1]);
+        acc.add(pa[0], tb[0]);
+      }
+      // T: the warp's 32 pieces of a term are 512 contiguous bytes of the record
+      const int row = lane & 15, half = lane >> 4;
+      uint8_t* out = rec + row_piece(16 * (pi - pj) + row, 8 * half);
+#pragma unroll
+      for (int u = 0; u < kTerms; ++u)
+        *reinterpret_cast<uint4*>(out + term_base(u) + (u == 2 ? tri_base(pj) : pair_base(pj))) =
+            *reinterpret_cast<const uint4*>(s.T[tri(pi, pj)][u] + piece);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        uint32_t t[kOutTerms];
+        split2(make_float2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1]), t);
+        uint8_t* o2 = rec + row_piece(127 - 16 * (pi + pj) - r4 - 8 * (z & 1), 8 * (z >> 1) + j2) + pair_base(pj);
+        *reinterpret_cast<uint32_t*>(o2 + term_base(0)) = t[0];
+        *reinterpret_cast<uint32_t*>(o2 + term_base(1)) = t[1];
       }
     }
   }

@@ -11,7 +11,7 @@
 //     D1 = S^T [q; k]^T         (A: S^T,  B: the q and k tiles as TMA left them)
 //     D2 = r^T [T; P T]^T       (A: r^T,  B: the prepared block)
 //     D3 = (e^(G63 - G) u)^T k  (A: u^T,  B: the k tile again, read the other way)
-// with r = v - e^G D1k, u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
+// with r = beta (v - e^G D1k), u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
 // fp32 by the threads. S, r and u are split into three bf16 terms (T and P T
 // are stored so), k and q are bf16 already: D1 and D3 take three products,
 // D2 the six largest of nine, smallest first, so that every result is
@@ -286,13 +286,17 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       tc_after();
       if (elect_one()) {
         const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
-        constexpr int pr[6] = {2, 0, 1, 1, 0, 0}, pt[6] = {0, 2, 1, 0, 1, 0};  // terms of r and of T, smallest first
+        // rows 16 kk .. 63 of T and P T see columns 16 kk .. 16 kk + 15. Terms of r and of T: the six largest
+        // products for T, the largest last; P T joins three of them, the first of which sets the accumulators
+        constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
 #pragma unroll
         for (int x = 0; x < 6; ++x)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15
-            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk, prep + (pt[x] * kTermBytes + tri_base(kk)) / 16,
-                   mma_desc(128 - 32 * kk, false), x > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
+            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk, b,
+                   mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || kk > 0);
+          }
         tc_commit(&ctl.d2);
       }
       __syncwarp();
@@ -337,21 +341,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         sqk::fence_proxy_async_smem();
       }
       const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 32 * half * 128 + col;
-      const float* coef = reinterpret_cast<const float*>(stage + kStagePrep + kTerms * kTermBytes);
+      const float* coef = reinterpret_cast<const float*>(stage + kStagePrep + kTermsBytes);
       const float4* eg = reinterpret_cast<const float4*>(coef + 32 * half);
-      const float4* ed = reinterpret_cast<const float4*>(coef + 64 + 32 * half);
+      const float4* eb = reinterpret_cast<const float4*>(coef + 64 + 32 * half);
+      const float4* ebg = reinterpret_cast<const float4*>(coef + 128 + 32 * half);
+      const float4* ed = reinterpret_cast<const float4*>(coef + 192 + 32 * half);
       const int mine = live - 32 * half;  // live rows of this half
       float x[32];
       uint32_t w[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = j < mine ? __bfloat162float(v[j * 128]) : 0.0f;
+      for (int j = 0; j < 32; j += 4) {
+        const float4 e = eb[j >> 2];
+        x[j] = j < mine ? e.x * __bfloat162float(v[j * 128]) : 0.0f;
+        x[j + 1] = j + 1 < mine ? e.y * __bfloat162float(v[(j + 1) * 128]) : 0.0f;
+        x[j + 2] = j + 2 < mine ? e.z * __bfloat162float(v[(j + 2) * 128]) : 0.0f;
+        x[j + 3] = j + 3 < mine ? e.w * __bfloat162float(v[(j + 3) * 128]) : 0.0f;
+      }
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
       tc_ld32(w, tl + TM_D1 + 64 + 32 * half);
       tc_wait_ld(w);
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
-        const float4 e = eg[j >> 2];
+        const float4 e = ebg[j >> 2];
         x[j] = j < mine ? fmaf(-e.x, __uint_as_float(w[j]), x[j]) : 0.0f;
         x[j + 1] = j + 1 < mine ? fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]) : 0.0f;
         x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
@@ -414,7 +426,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           sqk::bulk_commit();
         }
       }
-      const float g63 = coef[128];
+      const float g63 = coef[256];
       if (!warp_wait(ctl, &ctl.d3, ph, ns)) break;
       tc_after();
 #pragma unroll
