@@ -23,7 +23,7 @@
 // from and stored as two (2^-16). Only the blocks on and below the diagonal
 // are stored, in the order the scan's matrix instructions read them.
 // Bound by latency: a value head is a chain of six short phases with a
-// barrier between them, and four CTAs per SM run theirs against each other.
+// barrier between them, and five CTAs per SM run theirs against each other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -116,7 +116,6 @@ struct PrepGate {
   float from[64];    // e^(G_i - R_(b-1))  from its 16's start
   float to[64];      // e^(R_b - G_j)      to its 16's end
   float hop[4][4];   // e^(R_(bi-1) - R_bj), bj < bi
-  float diag[4][16][20];  // e^(G_i - G_j) inside the 16s, 0 above the diagonal
 };
 struct PrepSmem {
   union {
@@ -124,10 +123,10 @@ struct PrepSmem {
     struct {
       uint8_t A[6][kTerms][kBlk];       // blocks below the diagonal
       uint8_t P[10][kOutTerms][kBlk];   // blocks on and below it
+      uint8_t T[10][kTerms][kBlk];
       float Ad[4][16][20];              // A's blocks on it
     } m;
   };
-  uint8_t T[10][kTerms][kBlk];
   PrepGate gate[2];  // two value heads at a time
   float2 part[4];    // log gates summed by each warp
 };
@@ -240,9 +239,6 @@ __device__ __forceinline__ void prepare_gates(const PrepArgs& a, PrepSmem& sm, u
   s.beta[i] = beta;
   s.from[i] = pow2(pair_diff(G, prev));
   s.to[i] = pow2(pair_diff(mine, G));
-  const float2* G16 = s.G + (i & ~15);
-#pragma unroll 4
-  for (int j = 0; j < 16; ++j) s.diag[i >> 4][i & 15][j] = j <= (i & 15) ? pow2(pair_diff(G, G16[j])) : 0.0f;
   const int bi = (i >> 2) & 3, bj = i & 3;
   if (i < 16 && bj < bi) s.hop[bi][bj] = pow2(pair_diff(s.G[16 * bi - 1], s.G[16 * bj + 15]));
   if (on) {
@@ -258,7 +254,7 @@ __device__ __forceinline__ void prepare_gates(const PrepArgs& a, PrepSmem& sm, u
 
 // One CTA per block and key head; the value heads that share the key head
 // share q . k and k . k.
-__global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int c = blockIdx.x / a.r.h_k, hk = blockIdx.x - c * a.r.h_k;
@@ -310,19 +306,22 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
       for (int y = 0; y < 2; ++y) {
         const int i = 16 * bi + r4 + 8 * y;
         float f = which ? gt.beta[i] : 1.0f;
-        const float* col;
+        float t[4];  // of columns j2, + 1, + 8, + 9
         if (bi == bj) {
-          col = gt.diag[bi][r4 + 8 * y];
+          const float2 G = gt.G[i];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int lj = j2 + (z & 1) + 8 * (z >> 1);
+            t[z] = lj <= r4 + 8 * y ? pow2(pair_diff(G, gt.G[16 * bj + lj])) : 0.0f;
+          }
         } else {
-          col = gt.to + 16 * bj;
+          const float2 t0 = *reinterpret_cast<const float2*>(gt.to + 16 * bj + j2);
+          const float2 t1 = *reinterpret_cast<const float2*>(gt.to + 16 * bj + j2 + 8);
+          t[0] = t0.x, t[1] = t0.y, t[2] = t1.x, t[3] = t1.y;
           f *= gt.from[i] * gt.hop[bi][bj];
         }
-        const float2 t0 = *reinterpret_cast<const float2*>(col + j2);
-        const float2 t1 = *reinterpret_cast<const float2*>(col + j2 + 8);
-        m.c[0][2 * y] = f * t0.x * dot[x].c[0][2 * y];
-        m.c[0][2 * y + 1] = f * t0.y * dot[x].c[0][2 * y + 1];
-        m.c[1][2 * y] = f * t1.x * dot[x].c[1][2 * y];
-        m.c[1][2 * y + 1] = f * t1.y * dot[x].c[1][2 * y + 1];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) m.c[z >> 1][2 * y + (z & 1)] = f * t[z] * dot[x].c[z >> 1][2 * y + (z & 1)];
       }
       if (which && bi == bj) {
 #pragma unroll
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
         for (int l = 0; l < i; ++l) acc = fmaf(-Ad[i][l], t[l], acc);
         t[i] = acc;
       }
-      uint8_t* dst = s.T[tri(warp, warp)][0] + 2 * (col & 7);
+      uint8_t* dst = s.m.T[tri(warp, warp)][0] + 2 * (col & 7);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {  // each half warp stores eight rows
         float v = half ? t[8 + i] : t[i];
@@ -382,14 +381,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
         for (int m = m0; m <= R; ++m) {
 #pragma unroll
           for (int u = 0; u < kTerms; ++u) {
-            ldmatrix4(ta[u], s.T[tri(R, m)][u] + piece);
+            ldmatrix4(ta[u], s.m.T[tri(R, m)][u] + piece);
             ldmatrix4t(tb[u], s.m.A[below(m, l)][u] + piece);
           }
           add6(y, ta, tb);
         }
         acc_terms(y, ta);
 #pragma unroll
-        for (int u = 0; u < kTerms; ++u) ldmatrix4t(tb[u], s.T[tri(l, C)][u] + piece);
+        for (int u = 0; u < kTerms; ++u) ldmatrix4t(tb[u], s.m.T[tri(l, C)][u] + piece);
         add6(acc, ta, tb);
       }
 #pragma unroll
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
       }
       acc_terms(acc, ta);
 #pragma unroll
-      for (int u = 0; u < kTerms; ++u) put_left(s.T[tri(R, C)][u], ta[u]);
+      for (int u = 0; u < kTerms; ++u) put_left(s.m.T[tri(R, C)][u], ta[u]);
     }
     __syncthreads();
     // P T: five block products for each warp; T and P T leave
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
 #pragma unroll
         for (int u = 0; u < kOutTerms; ++u) {
           ldmatrix4(pa[u], s.m.P[tri(pi, l)][u] + piece);
-          ldmatrix4t(tb[u], s.T[tri(l, pj)][u] + piece);
+          ldmatrix4t(tb[u], s.m.T[tri(l, pj)][u] + piece);
         }
         acc.add(pa[1], tb[0]);
         acc.add(pa[0], tb[1]);
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_chunk_prepare(const PrepArg
 #pragma unroll
       for (int u = 0; u < kTerms; ++u)
         *reinterpret_cast<uint4*>(out + term_base(u) + (u == 2 ? tri_base(pj) : pair_base(pj))) =
-            *reinterpret_cast<const uint4*>(s.T[tri(pi, pj)][u] + piece);
+            *reinterpret_cast<const uint4*>(s.m.T[tri(pi, pj)][u] + piece);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         uint32_t t[kOutTerms];
