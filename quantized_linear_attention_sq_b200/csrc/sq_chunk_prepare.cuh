@@ -93,12 +93,17 @@ __device__ __forceinline__ void split3(float2 x, uint32_t (&t)[kTerms]) {
   const float2 lo = __ffma2_rn(mid, make_float2(-1.0f, -1.0f), r);
   t[2] = pack_high(lo.x, lo.y);
 }
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // rounded to nearest
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
 // The first two terms only, the second rounded to nearest.
 __device__ __forceinline__ void split2(float2 x, uint32_t* t) {
   const float2 hi = cut(x);
   t[0] = pack_high(hi.x, hi.y);
   const float2 r = __ffma2_rn(hi, make_float2(-1.0f, -1.0f), x);
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(t[1]) : "f"(r.y), "f"(r.x));
+  t[1] = bf16x2(r.x, r.y);
 }
 
 constexpr int kPrepThreads = 128;

@@ -13,17 +13,19 @@
 //     D3 = (e^(G63 - G) u)^T k  (A: u^T,  B: the k tile again, read the other way)
 // with r = beta (v - e^G D1k), u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
 // fp32 by the threads. S, r and u are split into three bf16 terms (T and P T
-// are stored so), k and q are bf16 already: D1 and D3 take three products,
-// D2 the six largest of nine, smallest first, so that every result is
-// fp32-accurate. The state adds one fresh accumulator per block in fp32:
+// are stored so), k and q are bf16 already: D1k and D3 take three products,
+// D2 the six largest of nine, so that the state is fp32-accurate; what only
+// reaches o, which is bf16, takes two terms (D1q) and three products (the P T
+// half of D2): 2^-16. The state adds one fresh accumulator per block in fp32:
 // the tensor core never accumulates across blocks.
 //
 // Ten warps: eight compute (two per 32 lanes of tensor memory, sharing the
-// columns), one issues the TMA loads of the next block, one the matrix
-// products. The chain of a block is D1 -> r -> D2 -> u -> D3 -> S; o is
-// finished under D3 and leaves by TMA from shared memory. An instruction of
-// the tensor core costs about the same for 64 and for 128 result columns, so
-// q and k, and T and P T, share theirs.
+// columns), one moves (TMA loads of the next block, stores of o), one issues
+// the matrix products. The chain of a block is D1k -> r -> D2 -> u -> D3 ->
+// S; its links overlap by halves: the products over the first half of a
+// thread's S, r or u start while it splits the second, and D3 is handed over
+// in two halves of the key rows. The q product runs under r, o is finished
+// under D3 and leaves under the next D1.
 #pragma once
 
 #include <cuda.h>
@@ -46,7 +48,8 @@ constexpr uint32_t kOutAt = kScanStages * kStageBytes;  // o rows on their way o
 
 struct ScanCtl {
   uint64_t full[kScanStages], empty[kScanStages];
-  uint64_t s_ready, r_ready, u_ready, o_ready, d1, d2, d3, drain;
+  uint64_t s_ready[2], r_ready[2], u_ready[2], d3[2];
+  uint64_t d1, d2, o_ready, o_free, drain;
   uint32_t tmem;
   int32_t abort;
 };
@@ -57,16 +60,16 @@ struct ScanArgs {
   uint64_t wait_ns;
 };
 
-// Columns of tensor memory (512, all of it).
-constexpr uint32_t TM_S = 0;      // S^T terms: hi and mid of key rows 0..63, of 64..127, then lo; D3 takes 0..127
-constexpr uint32_t TM_U = 128;    // u^T terms (over the lo terms of S^T)
-constexpr uint32_t TM_R = 224;    // r^T terms
-constexpr uint32_t TM_D1 = 320;   // S^T q^T, then S^T k^T
-constexpr uint32_t TM_D2 = 384;   // u^T (over S^T k^T), then the P T part of o, rows backwards
+// Columns of tensor memory (480 of 512).
+constexpr uint32_t TM_S = 0;      // S^T terms hi and mid, over D3: 32 columns for each 32 key rows; lo from 128 on
+constexpr uint32_t TM_RU = 192;   // r^T terms, then u^T terms
+constexpr uint32_t TM_D1Q = 288;  // S^T q^T
+constexpr uint32_t TM_D1K = 352;  // S^T k^T
+constexpr uint32_t TM_D2 = 352;   // u^T (over S^T k^T), then the P T part of o, rows backwards
 
 // Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
 __host__ __device__ constexpr uint32_t s_col(int s, int ks) {
-  return s == 2 ? 128u + 8u * ks : 64u * (ks >> 2) + 32u * s + 8u * (ks & 3);
+  return s == 2 ? 128u + 8u * ks : 32u * (ks >> 1) + 16u * s + 8u * (ks & 1);
 }
 
 // ---------------------------------------------------------- instructions
@@ -133,22 +136,19 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
          (1ull << 46) | (swizzle << 61);
 }
 
-// 32 fp32 values of a lane (k index 0..31 of an A operand) to tensor memory as three terms.
-template <typename Col>
-__device__ __forceinline__ void put_terms(const float (&x)[32], uint32_t base, Col col) {
+// 16 fp32 values of a lane (k index 0..15 of an A operand) to tensor memory as three terms.
+__device__ __forceinline__ void put_terms(const float* x, uint32_t hi, uint32_t mid, uint32_t lo) {
+  uint32_t t[kTerms][8];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    uint32_t t[kTerms][8];
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[kTerms];
+    split3(make_float2(x[2 * i], x[2 * i + 1]), w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[kTerms];
-      split3(make_float2(x[16 * p + 2 * i], x[16 * p + 2 * i + 1]), w);
-#pragma unroll
-      for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
-    }
-#pragma unroll
-    for (int s = 0; s < kTerms; ++s) tc_st8(base + col(s) + 8 * p, t[s]);
+    for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
   }
+  tc_st8(hi, t[0]);
+  tc_st8(mid, t[1]);
+  tc_st8(lo, t[2]);
 }
 
 // A warp's arrival on a barrier once its tensor memory stores are done.
@@ -197,17 +197,19 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   float* S_pool = reinterpret_cast<float*>(a.pool) + ((size_t)slot * a.h_v + h) * 128 * 128;
 
   if (tid == 0) {
-    for (int x = 0; x < kScanStages; ++x) {
+    constexpr uint32_t warps = kScanCompute / 32;
+    for (int x = 0; x < 2; ++x) {
       sqk::mbar_init(&ctl.full[x], 1);
-      sqk::mbar_init(&ctl.empty[x], kScanCompute / 32);
+      sqk::mbar_init(&ctl.empty[x], warps);
+      sqk::mbar_init(&ctl.s_ready[x], warps);
+      sqk::mbar_init(&ctl.r_ready[x], warps);
+      sqk::mbar_init(&ctl.u_ready[x], warps);
+      sqk::mbar_init(&ctl.d3[x], 1);
     }
-    sqk::mbar_init(&ctl.s_ready, kScanCompute / 32);
-    sqk::mbar_init(&ctl.r_ready, kScanCompute / 32);
-    sqk::mbar_init(&ctl.u_ready, kScanCompute / 32);
-    sqk::mbar_init(&ctl.o_ready, kScanCompute / 32);
+    sqk::mbar_init(&ctl.o_ready, warps);
+    sqk::mbar_init(&ctl.o_free, 1);
     sqk::mbar_init(&ctl.d1, 1);
     sqk::mbar_init(&ctl.d2, 1);
-    sqk::mbar_init(&ctl.d3, 1);
     sqk::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     sqk::fence_mbar_init();
@@ -218,18 +220,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // S^T: value column of this thread's lane, key rows 64 half .. 64 half + 63
+  // S^T: value column of this thread's lane; S[y][j] is key row 64 y + 32 half + j
   const int half = warp >> 2, col = (warp & 3) * 32 + lane;  // compute warps
   float S[2][32];
   if (warp < 8) {
-    const float* src = S_pool + (size_t)(64 * half) * 128 + col;
+    const float* src = S_pool + (size_t)(32 * half) * 128 + col;
     if (PACKED && resume) {
       float* Ssh = reinterpret_cast<float*>(smem);
       unpack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
-      src = Ssh + (64 * half) * 128 + col;
+      src = Ssh + (32 * half) * 128 + col;
     }
 #pragma unroll
-    for (int x = 0; x < 64; ++x) S[x >> 5][x & 31] = resume ? src[x * 128] : 0.0f;
+    for (int x = 0; x < 64; ++x) S[x >> 5][x & 31] = resume ? src[(64 * (x >> 5) + (x & 31)) * 128] : 0.0f;
     if (PACKED && resume) sqk::fence_proxy_async_smem();  // before TMA writes where S was read
   }
   tc_before();
@@ -239,80 +241,130 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const uint64_t ns = args.wait_ns;
   uint32_t st = 0;
 
-  if (warp == 8) {  // ---------------------------------------------- loads
+  if (warp == 8) {  // ------------------------------------- loads and stores
     if (lane == 0) {
       int issued = 0;
-      for (int i = 0; i < blocks; ++i) {
+      auto load = [&](int i) {
         const int sg = i & 1;
-        if (i >= kScanStages && !sqk::mbar_wait_bounded(&ctl.empty[sg], ((i >> 1) - 1) & 1, ns)) {
-          ctl.abort = 1;
-          break;
-        }
         uint8_t* stage = smem + sg * kStageBytes;
         sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx);
         const int row = first + 64 * i;
-        tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
         tma_tile(stage + kTileBytes / 2, &k_map, 0, hk, row, &ctl.full[sg]);
-        tma_tile(stage + kTileBytes, &q_map, 64, hk, row, &ctl.full[sg]);
         tma_tile(stage + 3 * kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
+        tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
+        tma_tile(stage + kTileBytes, &q_map, 64, hk, row, &ctl.full[sg]);
         tma_tile(stage + kStageV, &v_map, 0, h, row, &ctl.full[sg]);
         sqk::bulk_g2s(stage + kStagePrep, args.p.ws + ((uint64_t)(c0 + i) * a.h_v + h) * kPrepBytes, kPrepBytes,
                       &ctl.full[sg]);
         issued = i + 1;
+      };
+      load(0);
+      if (blocks > 1) load(1);
+      for (int i = 0; i < blocks; ++i) {
+        // block i's stage is free when its D3 is done; its o follows
+        if (i + kScanStages < blocks) {
+          if (!sqk::mbar_wait_bounded(&ctl.empty[i & 1], (i >> 1) & 1, ns)) {
+            ctl.abort = 1;
+            break;
+          }
+          load(i + kScanStages);
+        }
+        if (!sqk::mbar_wait_bounded(&ctl.o_ready, i & 1, ns)) {
+          ctl.abort = 1;
+          break;
+        }
+        const int live = n - 64 * i;
+        if (live >= 64) {
+          tma_store(&o_map, 0, h, first + 64 * i, smem + kOutAt);
+          sqk::bulk_commit();
+          sqk::bulk_wait_read_all();
+        } else {  // the last block: its live rows only
+          for (int y = 0; y < live; ++y)
+            sqk::bulk_s2g(out + ((size_t)(first + 64 * i + y) * a.h_v + h) * 128, smem + kOutAt + 256 * y, 256);
+          sqk::bulk_commit();
+        }
+        sqk::mbar_arrive(&ctl.o_free);
       }
       // no copy is in flight when the CTA ends
       for (int i = max(0, issued - kScanStages); i < issued; ++i)
         sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
+      sqk::bulk_wait_all();
     }
   } else if (warp == 9) {  // ------------------------------------- products
     const uint32_t base = sqk::smem_u32(smem);
     for (int i = 0; i < blocks; ++i) {
       const uint32_t ph = i & 1;
       const uint32_t stage = base + (i & 1) * kStageBytes;
-      if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns) || !warp_wait(ctl, &ctl.s_ready, ph, ns)) break;
-      tc_after();
-      if (elect_one()) {
-        const uint64_t qk = smem_desc(stage, 16, 1024, 2);
+      const uint64_t qt = smem_desc(stage, 16, 1024, 2), kt = qt + kTileBytes / 32;
+      if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int y = 0; y < 2 && ok; ++y) {  // k: the key rows 64 y .. 64 y + 63
+        ok = warp_wait(ctl, &ctl.s_ready[y], ph, ns);
+        tc_after();
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int s = kTerms - 1; s >= 0; --s)
+          for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma(tm + TM_D1K, tm + TM_S + s_col(s, ks) + (s == 2 ? 32 : 64) * y, kt + y * kTileBytes / 16 + ks * 2,
+                     mma_desc(64, false), s < kTerms - 1 || ks > 0 || y > 0);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) {
+        tc_commit(&ctl.d1);
+#pragma unroll
+        for (int s = 1; s >= 0; --s)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc_mma(tm + TM_D1, tm + TM_S + s_col(s, ks), qk + ((ks >> 2) * kTileBytes + (ks & 3) * 32) / 16,
-                   mma_desc(128, false), s < kTerms - 1 || ks > 0);
-        tc_commit(&ctl.d1);
+            tc_mma(tm + TM_D1Q, tm + TM_S + s_col(s, ks), qt + ((ks >> 2) * kTileBytes + (ks & 3) * 32) / 16,
+                   mma_desc(64, false), s < 1 || ks > 0);
       }
       __syncwarp();
-      if (!warp_wait(ctl, &ctl.r_ready, ph, ns)) break;
-      tc_after();
-      if (elect_one()) {
-        const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
-        // rows 16 kk .. 63 of T and P T see columns 16 kk .. 16 kk + 15. Terms of r and of T: the six largest
-        // products for T, the largest last; P T joins three of them, the first of which sets the accumulators
-        constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
+      // rows 16 kk .. 63 of T and P T see columns 16 kk .. 16 kk + 15. Terms of r and of T: the six largest products
+      // for T, the largest last; P T joins three of them, the first of which sets the accumulators
+#pragma unroll 1
+      for (int y = 0; y < 2 && ok; ++y) {  // kk = y and y + 2
+        ok = warp_wait(ctl, &ctl.r_ready[y], ph, ns);
+        tc_after();
+        if (ok && elect_one()) {
+          const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
+          constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
 #pragma unroll
-        for (int x = 0; x < 6; ++x)
+          for (int x = 0; x < 6; ++x)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
-            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk, b,
-                   mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || kk > 0);
+            for (int z = 0; z < 2; ++z) {
+              const int kk = 2 * z + y;
+              const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
+              tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk, b,
+                     mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || z > 0 || y > 0);
+            }
+          if (y == 1) tc_commit(&ctl.d2);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int y = 0; y < 2 && ok; ++y) {  // rows 16 y .. + 15 and 16 (y + 2) .. + 15 of u and k
+        ok = warp_wait(ctl, &ctl.u_ready[y], ph, ns);
+        tc_after();
+        if (ok && elect_one()) {
+          const uint64_t km = smem_desc(stage + kTileBytes / 2, kTileBytes, 1024, 2) + y * 128;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // key rows 64 x .. 64 x + 63
+#pragma unroll
+            for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+              for (int z = 0; z < 2; ++z)
+                tc_mma(tm + TM_S + 64 * x, tm + TM_RU + 32 * s + 16 * z + 8 * y, km + (x * kTileBytes + z * 4096) / 16,
+                       mma_desc(64, true), s < kTerms - 1 || z > 0 || y > 0);
+            if (y == 1) tc_commit(&ctl.d3[x]);
           }
-        tc_commit(&ctl.d2);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (!warp_wait(ctl, &ctl.u_ready, ph, ns)) break;
-      tc_after();
-      if (elect_one()) {
-        const uint64_t kt = smem_desc(stage + kTileBytes / 2, kTileBytes, 1024, 2);
-#pragma unroll
-        for (int s = kTerms - 1; s >= 0; --s)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tm + TM_S, tm + TM_U + 32 * s + 8 * ks, kt + ks * 2048 / 16, mma_desc(128, true),
-                   s < kTerms - 1 || ks > 0);
-        tc_commit(&ctl.d3);
-      }
-      __syncwarp();
+      if (!ok) break;
     }
     // no product is in flight when the tensor memory is given back
     if (elect_one()) tc_commit(&ctl.drain);
@@ -320,13 +372,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     warp_wait(ctl, &ctl.drain, 0, ns);
   } else {  // -------------------------------------------------- the rest
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    auto put_state = [&]() {
+    auto put_state = [&](int y) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        put_terms(S[x], tl + TM_S, [&](int s) { return s_col(s, 4 * half + 2 * x); });
-      warp_arrive(&ctl.s_ready);
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t hi = tl + TM_S + 64 * y + 32 * half + 8 * z;
+        put_terms(S[y] + 16 * z, hi, hi + 16, tl + TM_S + 128 + 32 * y + 16 * half + 8 * z);
+      }
+      warp_arrive(&ctl.s_ready[y]);
     };
-    put_state();
+    put_state(0);
+    put_state(1);
     for (int i = 0; i < blocks; ++i) {
       const int sg = i & 1;
       const uint32_t ph = i & 1;
@@ -359,79 +414,70 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
-      tc_ld32(w, tl + TM_D1 + 64 + 32 * half);
+      tc_ld32(w, tl + TM_D1K + 32 * half);
       tc_wait_ld(w);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 e = ebg[j >> 2];
-        x[j] = j < mine ? fmaf(-e.x, __uint_as_float(w[j]), x[j]) : 0.0f;
-        x[j + 1] = j + 1 < mine ? fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]) : 0.0f;
-        x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
-        x[j + 3] = j + 3 < mine ? fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]) : 0.0f;
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int j = 16 * y; j < 16 * y + 16; j += 4) {
+          const float4 e = ebg[j >> 2];
+          x[j] = j < mine ? fmaf(-e.x, __uint_as_float(w[j]), x[j]) : 0.0f;
+          x[j + 1] = j + 1 < mine ? fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]) : 0.0f;
+          x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
+          x[j + 3] = j + 3 < mine ? fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]) : 0.0f;
+        }
+        const uint32_t to = tl + TM_RU + 16 * half + 8 * y;
+        put_terms(x + 16 * y, to, to + 32, to + 64);
+        warp_arrive(&ctl.r_ready[y]);
       }
-      // the block before's o has left its staging rows: this warp's arrival leads to the next D2, before which no
-      // other warp writes there
-      if (tid == 0) sqk::bulk_wait_read_all();
-      __syncwarp();
-      put_terms(x, tl + TM_R + 16 * half, [](int s) { return 32u * s; });
-      warp_arrive(&ctl.r_ready);
 
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
       tc_after();
       tc_ld32(w, tl + TM_D2 + 32 * half);
       tc_wait_ld(w);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 e = ed[j >> 2];
-        x[j] = e.x * __uint_as_float(w[j]);
-        x[j + 1] = e.y * __uint_as_float(w[j + 1]);
-        x[j + 2] = e.z * __uint_as_float(w[j + 2]);
-        x[j + 3] = e.w * __uint_as_float(w[j + 3]);
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int j = 16 * y; j < 16 * y + 16; j += 4) {
+          const float4 e = ed[j >> 2];
+          x[j] = e.x * __uint_as_float(w[j]);
+          x[j + 1] = e.y * __uint_as_float(w[j + 1]);
+          x[j + 2] = e.z * __uint_as_float(w[j + 2]);
+          x[j + 3] = e.w * __uint_as_float(w[j + 3]);
+        }
+        const uint32_t to = tl + TM_RU + 16 * half + 8 * y;
+        put_terms(x + 16 * y, to, to + 32, to + 64);
+        warp_arrive(&ctl.u_ready[y]);
       }
-      put_terms(x, tl + TM_U + 16 * half, [](int s) { return 32u * s; });
-      warp_arrive(&ctl.u_ready);
 
       // o, under the state's product
+      uint32_t o2[16];
       {
         uint32_t y[32];
-        tc_ld32(w, tl + TM_D1 + 32 * half);
+        tc_ld32(w, tl + TM_D1Q + 32 * half);
         tc_ld32(y, tl + TM_D2 + 96 - 32 * half);
         tc_wait_ld(w);
         tc_wait_ld(y);
-        __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(smem + kOutAt) + 32 * half * 128 + col;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 e4 = eg[j >> 2];
-          const float e[4] = {e4.x, e4.y, e4.z, e4.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float o = fmaf(e[k], __uint_as_float(w[j + k]), __uint_as_float(y[31 - j - k]));
-            if (o != o && j + k < mine) st |= ST_NAN;
-            op[(j + k) * 128] = __float2bfloat16_rn(o);
-          }
-        }
-      }
-      sqk::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
-      if (live < 64) {  // the last block: its live rows only
-        if (!warp_wait(ctl, &ctl.o_ready, ph, ns)) break;
-        for (int y = tid; y < live * 16; y += kScanCompute)
-          reinterpret_cast<uint4*>(out + ((size_t)(first + 64 * i + (y >> 4)) * a.h_v + h) * 128)[y & 15] =
-              reinterpret_cast<const uint4*>(smem + kOutAt)[y];
-      } else if (warp == 0) {
-        if (!warp_wait(ctl, &ctl.o_ready, ph, ns)) break;
-        if (lane == 0) {
-          tma_store(&o_map, 0, h, first + 64 * i, smem + kOutAt);
-          sqk::bulk_commit();
+          const float4 e = eg[j >> 2];
+          const float p0 = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[31 - j]));
+          const float p1 = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[30 - j]));
+          const float p2 = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[29 - j]));
+          const float p3 = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[28 - j]));
+          o2[j >> 1] = bf16x2(p0, p1);
+          o2[(j >> 1) + 1] = bf16x2(p2, p3);
         }
       }
       const float g63 = coef[256];
-      if (!warp_wait(ctl, &ctl.d3, ph, ns)) break;
-      tc_after();
+      bool ok = true;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        tc_ld32(w, tl + TM_S + 64 * half + 32 * y);
+        ok = ok && warp_wait(ctl, &ctl.d3[y], ph, ns);
+        if (!ok) break;
+        tc_after();
+        if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before
+        tc_ld32(w, tl + TM_S + 64 * y + 32 * half);
         tc_wait_ld(w);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
@@ -440,12 +486,24 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           S[y][j] = t.x;
           S[y][j + 1] = t.y;
         }
+        if (i + 1 < blocks) put_state(y);
       }
-      if (lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before the loads above
-      if (i + 1 < blocks) put_state();
+      if (!ok) break;
+      // o's rows go out while the next block's first product runs
+      if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
+      uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 32 * half * 128 + col;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const uint32_t t = o2[j >> 1];
+        op[j * 128] = (uint16_t)t;
+        op[(j + 1) * 128] = (uint16_t)(t >> 16);
+        if (((t & 0x7fffu) > 0x7f80u && j < mine) || ((t & 0x7fffffffu) > 0x7f80ffffu && j + 1 < mine)) st |= ST_NAN;
+      }
+      sqk::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
     }
   }
-  if (tid == 0) sqk::bulk_wait_all();
   tc_before();
   __syncthreads();
   tc_after();
@@ -459,12 +517,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     if (PACKED) {
       float* Ssh = reinterpret_cast<float*>(smem);
 #pragma unroll
-      for (int x = 0; x < 64; ++x) Ssh[(64 * half + x) * 128 + col] = S[x >> 5][x & 31];
+      for (int x = 0; x < 64; ++x) Ssh[(64 * (x >> 5) + 32 * half + (x & 31)) * 128 + col] = S[x >> 5][x & 31];
       st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
     } else {
-      float* dst = S_pool + (size_t)(64 * half) * 128 + col;
+      float* dst = S_pool + (size_t)(32 * half) * 128 + col;
 #pragma unroll
-      for (int x = 0; x < 64; ++x) dst[x * 128] = S[x >> 5][x & 31];
+      for (int x = 0; x < 64; ++x) dst[(64 * (x >> 5) + (x & 31)) * 128] = S[x >> 5][x & 31];
     }
     if (st) atomicOr(a.t.status, st);
   }
