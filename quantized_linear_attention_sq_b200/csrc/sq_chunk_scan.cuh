@@ -19,13 +19,12 @@
 // half of D2): 2^-16. The state adds one fresh accumulator per block in fp32:
 // the tensor core never accumulates across blocks.
 //
-// Ten warps: eight compute (two per 32 lanes of tensor memory, sharing the
-// columns), one moves (TMA loads of the next block, stores of o), one issues
-// the matrix products. The chain of a block is D1k -> r -> D2 -> u -> D3 ->
-// S; its links overlap by halves: the products over the first half of a
-// thread's S, r or u start while it splits the second, and D3 is handed over
-// in two halves of the key rows. The q product runs under r, o is finished
-// under D3 and leaves under the next D1.
+// Eighteen warps: sixteen compute (four per 32 lanes of tensor memory, sharing
+// the columns), one moves (TMA loads of the next block, stores of o), one
+// issues the matrix products. The chain of a block is D1k -> r -> D2 -> u ->
+// D3 -> S; D3 and S go by halves of the key rows, so that the second half of
+// D3 and the first of the next D1k run under S. The q product runs under r, o
+// is finished under D3 and leaves under the next D1k.
 #pragma once
 
 #include <cuda.h>
@@ -35,8 +34,9 @@
 
 namespace sqr {
 
-constexpr int kScanCompute = 256;             // threads that own a part of the state
+constexpr int kScanCompute = 512;             // threads that own a part of the state
 constexpr int kScanThreads = kScanCompute + 64;
+constexpr int kMoveWarp = kScanCompute / 32, kProductWarp = kMoveWarp + 1;
 constexpr int kScanStages = 2;
 constexpr uint32_t kTileBytes = 64 * 128 * 2;  // q, k, v or o rows of a block
 // A stage: channels 0..63 of the q rows, then of the k rows, the same for
@@ -48,8 +48,8 @@ constexpr uint32_t kOutAt = kScanStages * kStageBytes;  // o rows on their way o
 
 struct ScanCtl {
   uint64_t full[kScanStages], empty[kScanStages];
-  uint64_t s_ready[2], r_ready[2], u_ready[2], d3[2];
-  uint64_t d1, d2, o_ready, o_free, drain;
+  uint64_t s_ready[2], d3[2];
+  uint64_t r_ready, u_ready, d1, d2, o_ready, o_free, drain;
   uint32_t tmem;
   int32_t abort;
 };
@@ -61,7 +61,7 @@ struct ScanArgs {
 };
 
 // Columns of tensor memory (480 of 512).
-constexpr uint32_t TM_S = 0;      // S^T terms hi and mid, over D3: 32 columns for each 32 key rows; lo from 128 on
+constexpr uint32_t TM_S = 0;      // S^T terms hi and mid, over D3: 16 columns for each 16 key rows; lo from 128 on
 constexpr uint32_t TM_RU = 192;   // r^T terms, then u^T terms
 constexpr uint32_t TM_D1Q = 288;  // S^T q^T
 constexpr uint32_t TM_D1K = 352;  // S^T k^T
@@ -69,7 +69,7 @@ constexpr uint32_t TM_D2 = 352;   // u^T (over S^T k^T), then the P T part of o,
 
 // Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
 __host__ __device__ constexpr uint32_t s_col(int s, int ks) {
-  return s == 2 ? 128u + 8u * ks : 32u * (ks >> 1) + 16u * s + 8u * (ks & 1);
+  return s == 2 ? 128u + 8u * ks : 16u * ks + 8u * s;
 }
 
 // ---------------------------------------------------------- instructions
@@ -108,18 +108,17 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 #define SQ_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
 #define SQ_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
-__device__ __forceinline__ void tc_ld32(uint32_t (&x)[32], uint32_t addr) {
+__device__ __forceinline__ void tc_ld16(uint32_t (&x)[16], uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : SQ_R8(x, 0), SQ_R8(x, 8), SQ_R8(x, 16), SQ_R8(x, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SQ_R8(x, 0), SQ_R8(x, 8)
       : "r"(addr)
       : "memory");
 }
 // Waits for the loads; the values pass through it, so no use of them moves above.
 #define SQ_RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&x)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : SQ_RW8(x, 0), SQ_RW8(x, 8), SQ_RW8(x, 16), SQ_RW8(x, 24)::"memory");
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SQ_RW8(x, 0), SQ_RW8(x, 8)::"memory");
 }
 __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&x)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), SQ_W8(x, 0)
@@ -137,7 +136,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 }
 
 // 16 fp32 values of a lane (k index 0..15 of an A operand) to tensor memory as three terms.
-__device__ __forceinline__ void put_terms(const float* x, uint32_t hi, uint32_t mid, uint32_t lo) {
+__device__ __forceinline__ void put_terms(const float (&x)[16], uint32_t hi, uint32_t mid, uint32_t lo) {
   uint32_t t[kTerms][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -167,7 +166,8 @@ __device__ __forceinline__ bool warp_wait(ScanCtl& c, uint64_t* bar, uint32_t pa
   return false;
 }
 
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kScanCompute) : "memory"); }
+// The 256 threads of the record's thread map.
+__device__ __forceinline__ void record_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool PACKED>
 __global__ void __launch_bounds__(kScanThreads, 1)
@@ -202,10 +202,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       sqk::mbar_init(&ctl.full[x], 1);
       sqk::mbar_init(&ctl.empty[x], warps);
       sqk::mbar_init(&ctl.s_ready[x], warps);
-      sqk::mbar_init(&ctl.r_ready[x], warps);
-      sqk::mbar_init(&ctl.u_ready[x], warps);
       sqk::mbar_init(&ctl.d3[x], 1);
     }
+    sqk::mbar_init(&ctl.r_ready, warps);
+    sqk::mbar_init(&ctl.u_ready, warps);
     sqk::mbar_init(&ctl.o_ready, warps);
     sqk::mbar_init(&ctl.o_free, 1);
     sqk::mbar_init(&ctl.d1, 1);
@@ -214,24 +214,23 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     ctl.abort = 0;
     sqk::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sqk::smem_u32(&ctl.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // S^T: value column of this thread's lane; S[y][j] is key row 64 y + 32 half + j
-  const int half = warp >> 2, col = (warp & 3) * 32 + lane;  // compute warps
-  float S[2][32];
-  if (warp < 8) {
-    const float* src = S_pool + (size_t)(32 * half) * 128 + col;
-    if (PACKED && resume) {
-      float* Ssh = reinterpret_cast<float*>(smem);
-      unpack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
-      src = Ssh + (32 * half) * 128 + col;
-    }
+  // S^T: value column of this thread's lane; S[y][j] is key row 64 y + 16 part + j
+  const int part = warp >> 2, col = (warp & 3) * 32 + lane;  // compute warps
+  float S[2][16];
+  if (PACKED && resume) {
+    if (warp < 8) unpack_state<128>(a, h, record, smem + 128 * 128 * 4, reinterpret_cast<float*>(smem), record_sync);
+    __syncthreads();
+  }
+  if (warp < kMoveWarp) {
+    const float* src = (PACKED ? reinterpret_cast<const float*>(smem) : S_pool) + (size_t)(16 * part) * 128 + col;
 #pragma unroll
-    for (int x = 0; x < 64; ++x) S[x >> 5][x & 31] = resume ? src[(64 * (x >> 5) + (x & 31)) * 128] : 0.0f;
+    for (int x = 0; x < 32; ++x) S[x >> 4][x & 15] = resume ? src[(64 * (x >> 4) + (x & 15)) * 128] : 0.0f;
     if (PACKED && resume) sqk::fence_proxy_async_smem();  // before TMA writes where S was read
   }
   tc_before();
@@ -241,7 +240,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const uint64_t ns = args.wait_ns;
   uint32_t st = 0;
 
-  if (warp == 8) {  // ------------------------------------- loads and stores
+  if (warp == kMoveWarp) {  // ------------------------------------- loads and stores
     if (lane == 0) {
       int issued = 0;
       auto load = [&](int i) {
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
       sqk::bulk_wait_all();
     }
-  } else if (warp == 9) {  // ------------------------------------- products
+  } else if (warp == kProductWarp) {  // ------------------------------------- products
     const uint32_t base = sqk::smem_u32(smem);
     for (int i = 0; i < blocks; ++i) {
       const uint32_t ph = i & 1;
@@ -325,46 +324,38 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       __syncwarp();
       // rows 16 kk .. 63 of T and P T see columns 16 kk .. 16 kk + 15. Terms of r and of T: the six largest products
       // for T, the largest last; P T joins three of them, the first of which sets the accumulators
-#pragma unroll 1
-      for (int y = 0; y < 2 && ok; ++y) {  // kk = y and y + 2
-        ok = warp_wait(ctl, &ctl.r_ready[y], ph, ns);
-        tc_after();
-        if (ok && elect_one()) {
-          const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
-          constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
+      if (!warp_wait(ctl, &ctl.r_ready, ph, ns)) break;
+      tc_after();
+      if (elect_one()) {
+        const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
+        constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
 #pragma unroll
-          for (int x = 0; x < 6; ++x)
+        for (int x = 0; x < 6; ++x)
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int kk = 2 * z + y;
-              const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
-              tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk, b,
-                     mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || z > 0 || y > 0);
-            }
-          if (y == 1) tc_commit(&ctl.d2);
-        }
-        __syncwarp();
-      }
-#pragma unroll 1
-      for (int y = 0; y < 2 && ok; ++y) {  // rows 16 y .. + 15 and 16 (y + 2) .. + 15 of u and k
-        ok = warp_wait(ctl, &ctl.u_ready[y], ph, ns);
-        tc_after();
-        if (ok && elect_one()) {
-          const uint64_t km = smem_desc(stage + kTileBytes / 2, kTileBytes, 1024, 2) + y * 128;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {  // key rows 64 x .. 64 x + 63
-#pragma unroll
-            for (int s = kTerms - 1; s >= 0; --s)
-#pragma unroll
-              for (int z = 0; z < 2; ++z)
-                tc_mma(tm + TM_S + 64 * x, tm + TM_RU + 32 * s + 16 * z + 8 * y, km + (x * kTileBytes + z * 4096) / 16,
-                       mma_desc(64, true), s < kTerms - 1 || z > 0 || y > 0);
-            if (y == 1) tc_commit(&ctl.d3[x]);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
+            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk, b,
+                   mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || kk > 0);
           }
-        }
-        __syncwarp();
+        tc_commit(&ctl.d2);
       }
-      if (!ok) break;
+      __syncwarp();
+      if (!warp_wait(ctl, &ctl.u_ready, ph, ns)) break;
+      tc_after();
+      if (elect_one()) {
+        const uint64_t km = smem_desc(stage + kTileBytes / 2, kTileBytes, 1024, 2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {  // key rows 64 x .. 64 x + 63
+#pragma unroll
+          for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma(tm + TM_S + 64 * x, tm + TM_RU + 32 * s + 8 * kk, km + (x * kTileBytes + kk * 2048) / 16,
+                     mma_desc(64, true), s < kTerms - 1 || kk > 0);
+          tc_commit(&ctl.d3[x]);
+        }
+      }
+      __syncwarp();
     }
     // no product is in flight when the tensor memory is given back
     if (elect_one()) tc_commit(&ctl.drain);
@@ -373,13 +364,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   } else {  // -------------------------------------------------- the rest
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     auto put_state = [&](int y) {
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const uint32_t hi = tl + TM_S + 64 * y + 32 * half + 8 * z;
-        put_terms(S[y] + 16 * z, hi, hi + 16, tl + TM_S + 128 + 32 * y + 16 * half + 8 * z);
-      }
+      const uint32_t hi = tl + TM_S + 64 * y + 16 * part;
+      put_terms(S[y], hi, hi + 8, tl + TM_S + 128 + 32 * y + 8 * part);
       warp_arrive(&ctl.s_ready[y]);
     };
+    const uint32_t ru = tl + TM_RU + 8 * part;  // r and u of rows 16 part .. + 15
     put_state(0);
     put_state(1);
     for (int i = 0; i < blocks; ++i) {
@@ -387,7 +376,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const uint32_t ph = i & 1;
       uint8_t* stage = smem + sg * kStageBytes;
       if (!warp_wait(ctl, &ctl.full[sg], (i >> 1) & 1, ns)) break;
-      const int live = min(64, n - 64 * i);
+      const int live = min(64, n - 64 * i), mine = live - 16 * part;  // rows; of this thread
       if (live < 64) {
         // rows of the k tile behind the request's last: another request's, or none's
         for (int x = tid; x < (64 - live) * 16; x += kScanCompute)
@@ -395,76 +384,70 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                                     (x & 7) * 16) = make_uint4(0, 0, 0, 0);
         sqk::fence_proxy_async_smem();
       }
-      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 32 * half * 128 + col;
+      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 16 * part * 128 + col;
       const float* coef = reinterpret_cast<const float*>(stage + kStagePrep + kTermsBytes);
-      const float4* eg = reinterpret_cast<const float4*>(coef + 32 * half);
-      const float4* eb = reinterpret_cast<const float4*>(coef + 64 + 32 * half);
-      const float4* ebg = reinterpret_cast<const float4*>(coef + 128 + 32 * half);
-      const float4* ed = reinterpret_cast<const float4*>(coef + 192 + 32 * half);
-      const int mine = live - 32 * half;  // live rows of this half
-      float x[32];
-      uint32_t w[32];
+      const float4* eg = reinterpret_cast<const float4*>(coef + 16 * part);  // e^G; 16 float4s on: beta, beta e^G, e^(G63 - G)
+      float x[16];
+      uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 e = eb[j >> 2];
-        x[j] = j < mine ? e.x * __bfloat162float(v[j * 128]) : 0.0f;
-        x[j + 1] = j + 1 < mine ? e.y * __bfloat162float(v[(j + 1) * 128]) : 0.0f;
-        x[j + 2] = j + 2 < mine ? e.z * __bfloat162float(v[(j + 2) * 128]) : 0.0f;
-        x[j + 3] = j + 3 < mine ? e.w * __bfloat162float(v[(j + 3) * 128]) : 0.0f;
+      for (int j = 0; j < 16; j += 4) {
+        const float4 e = eg[16 + (j >> 2)];
+        x[j] = e.x * __bfloat162float(v[j * 128]);
+        x[j + 1] = e.y * __bfloat162float(v[(j + 1) * 128]);
+        x[j + 2] = e.z * __bfloat162float(v[(j + 2) * 128]);
+        x[j + 3] = e.w * __bfloat162float(v[(j + 3) * 128]);
       }
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
-      tc_ld32(w, tl + TM_D1K + 32 * half);
+      tc_ld16(w, tl + TM_D1K + 16 * part);
       tc_wait_ld(w);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-#pragma unroll
-        for (int j = 16 * y; j < 16 * y + 16; j += 4) {
-          const float4 e = ebg[j >> 2];
-          x[j] = j < mine ? fmaf(-e.x, __uint_as_float(w[j]), x[j]) : 0.0f;
-          x[j + 1] = j + 1 < mine ? fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]) : 0.0f;
-          x[j + 2] = j + 2 < mine ? fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]) : 0.0f;
-          x[j + 3] = j + 3 < mine ? fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]) : 0.0f;
-        }
-        const uint32_t to = tl + TM_RU + 16 * half + 8 * y;
-        put_terms(x + 16 * y, to, to + 32, to + 64);
-        warp_arrive(&ctl.r_ready[y]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 e = eg[32 + (j >> 2)];
+        x[j] = fmaf(-e.x, __uint_as_float(w[j]), x[j]);
+        x[j + 1] = fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]);
+        x[j + 2] = fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]);
+        x[j + 3] = fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]);
       }
+      if (live < 64) {  // whatever the rows behind the last held
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = j < mine ? x[j] : 0.0f;
+      }
+      put_terms(x, ru, ru + 32, ru + 64);
+      warp_arrive(&ctl.r_ready);
 
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
       tc_after();
-      tc_ld32(w, tl + TM_D2 + 32 * half);
+      tc_ld16(w, tl + TM_D2 + 16 * part);
       tc_wait_ld(w);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-#pragma unroll
-        for (int j = 16 * y; j < 16 * y + 16; j += 4) {
-          const float4 e = ed[j >> 2];
-          x[j] = e.x * __uint_as_float(w[j]);
-          x[j + 1] = e.y * __uint_as_float(w[j + 1]);
-          x[j + 2] = e.z * __uint_as_float(w[j + 2]);
-          x[j + 3] = e.w * __uint_as_float(w[j + 3]);
-        }
-        const uint32_t to = tl + TM_RU + 16 * half + 8 * y;
-        put_terms(x + 16 * y, to, to + 32, to + 64);
-        warp_arrive(&ctl.u_ready[y]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 e = eg[48 + (j >> 2)];
+        x[j] = e.x * __uint_as_float(w[j]);
+        x[j + 1] = e.y * __uint_as_float(w[j + 1]);
+        x[j + 2] = e.z * __uint_as_float(w[j + 2]);
+        x[j + 3] = e.w * __uint_as_float(w[j + 3]);
       }
+      put_terms(x, ru, ru + 32, ru + 64);
+      warp_arrive(&ctl.u_ready);
 
       // o, under the state's product
-      uint32_t o2[16];
+      uint32_t o2[8];
+      float bad = 0.0f;  // stays 0 while every o is finite
       {
-        uint32_t y[32];
-        tc_ld32(w, tl + TM_D1Q + 32 * half);
-        tc_ld32(y, tl + TM_D2 + 96 - 32 * half);
+        uint32_t y[16];
+        tc_ld16(w, tl + TM_D1Q + 16 * part);
+        tc_ld16(y, tl + TM_D2 + 112 - 16 * part);
         tc_wait_ld(w);
         tc_wait_ld(y);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           const float4 e = eg[j >> 2];
-          const float p0 = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[31 - j]));
-          const float p1 = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[30 - j]));
-          const float p2 = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[29 - j]));
-          const float p3 = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[28 - j]));
+          const float p0 = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[15 - j]));
+          const float p1 = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[14 - j]));
+          const float p2 = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[13 - j]));
+          const float p3 = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[12 - j]));
+          bad = fmaf(p0, 0.0f, fmaf(p1, 0.0f, fmaf(p2, 0.0f, fmaf(p3, 0.0f, bad))));
           o2[j >> 1] = bf16x2(p0, p1);
           o2[(j >> 1) + 1] = bf16x2(p2, p3);
         }
@@ -477,10 +460,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         if (!ok) break;
         tc_after();
         if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before
-        tc_ld32(w, tl + TM_S + 64 * y + 32 * half);
+        tc_ld16(w, tl + TM_S + 64 * y + 16 * part);
         tc_wait_ld(w);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < 16; j += 2) {
           const float2 t = __ffma2_rn(make_float2(g63, g63), make_float2(S[y][j], S[y][j + 1]),
                                       make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])));
           S[y][j] = t.x;
@@ -491,13 +474,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (!ok) break;
       // o's rows go out while the next block's first product runs
       if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
-      uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 32 * half * 128 + col;
+      uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 16 * part * 128 + col;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const uint32_t t = o2[j >> 1];
-        op[j * 128] = (uint16_t)t;
-        op[(j + 1) * 128] = (uint16_t)(t >> 16);
-        if (((t & 0x7fffu) > 0x7f80u && j < mine) || ((t & 0x7fffffffu) > 0x7f80ffffu && j + 1 < mine)) st |= ST_NAN;
+      for (int j = 0; j < 16; j += 2) {
+        op[j * 128] = (uint16_t)o2[j >> 1];
+        op[(j + 1) * 128] = (uint16_t)(o2[j >> 1] >> 16);
+      }
+      if (bad != 0.0f) {  // an infinity or a NaN: a NaN in a live row is reported
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < mine && ((o2[j >> 1] >> (16 * (j & 1))) & 0x7fffu) > 0x7f80u) st |= ST_NAN;
       }
       sqk::fence_proxy_async_smem();
       __syncwarp();
@@ -507,25 +493,22 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 9)
+  if (warp == kProductWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
   if (ctl.abort) {  // the state in the pool stays as it was
     if (tid == 0) atomicOr(a.t.status, sqk::ST_TIMEOUT);
     return;
   }
-  if (warp < 8) {
-    if (PACKED) {
-      float* Ssh = reinterpret_cast<float*>(smem);
+  if (warp < kMoveWarp) {
+    float* dst = (PACKED ? reinterpret_cast<float*>(smem) : S_pool) + (size_t)(16 * part) * 128 + col;
 #pragma unroll
-      for (int x = 0; x < 64; ++x) Ssh[(64 * (x >> 5) + 32 * half + (x & 31)) * 128 + col] = S[x >> 5][x & 31];
-      st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, Ssh, compute_sync);
-    } else {
-      float* dst = S_pool + (size_t)(32 * half) * 128 + col;
-#pragma unroll
-      for (int x = 0; x < 64; ++x) dst[(64 * (x >> 5) + (x & 31)) * 128] = S[x >> 5][x & 31];
-    }
-    if (st) atomicOr(a.t.status, st);
+    for (int x = 0; x < 32; ++x) dst[(64 * (x >> 4) + (x & 15)) * 128] = S[x >> 4][x & 15];
   }
+  if (PACKED) {
+    __syncthreads();
+    if (warp < 8) st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, reinterpret_cast<float*>(smem), record_sync);
+  }
+  if (st) atomicOr(a.t.status, st);
 }
 
 }  // namespace sqr
