@@ -81,17 +81,13 @@ __device__ __forceinline__ bool block_span(const PrepArgs& a, int c, int& first,
 __device__ __forceinline__ uint32_t pack_high(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float2 cut(float2 x) {
-  return make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
-}
-__device__ __forceinline__ void split3(float2 x, uint32_t (&t)[kTerms]) {
-  const float2 hi = cut(x);
-  t[0] = pack_high(hi.x, hi.y);
-  const float2 r = __ffma2_rn(hi, make_float2(-1.0f, -1.0f), x);
-  const float2 mid = cut(r);
-  t[1] = pack_high(mid.x, mid.y);
-  const float2 lo = __ffma2_rn(mid, make_float2(-1.0f, -1.0f), r);
-  t[2] = pack_high(lo.x, lo.y);
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[kTerms]) {
+  t[0] = pack_high(a, b);
+  a = __fsub_rn(a, cut(a));
+  b = __fsub_rn(b, cut(b));
+  t[1] = pack_high(a, b);
+  t[2] = pack_high(__fsub_rn(a, cut(a)), __fsub_rn(b, cut(b)));
 }
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // rounded to nearest
   uint32_t r;
@@ -99,11 +95,9 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // rounded to ne
   return r;
 }
 // The first two terms only, the second rounded to nearest.
-__device__ __forceinline__ void split2(float2 x, uint32_t* t) {
-  const float2 hi = cut(x);
-  t[0] = pack_high(hi.x, hi.y);
-  const float2 r = __ffma2_rn(hi, make_float2(-1.0f, -1.0f), x);
-  t[1] = bf16x2(r.x, r.y);
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[kOutTerms]) {
+  t[0] = pack_high(a, b);
+  t[1] = bf16x2(__fsub_rn(a, cut(a)), __fsub_rn(b, cut(b)));
 }
 
 constexpr int kPrepThreads = 128;
@@ -182,7 +176,7 @@ __device__ __forceinline__ void acc_terms(const Acc& acc, Terms& t) {
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     uint32_t w[kTerms];
-    split3(make_float2(acc.c[x >> 1][2 * (x & 1)], acc.c[x >> 1][2 * (x & 1) + 1]), w);
+    split3(acc.c[x >> 1][2 * (x & 1)], acc.c[x >> 1][2 * (x & 1) + 1], w);
 #pragma unroll
     for (int s = 0; s < kTerms; ++s) t[s][x] = w[s];
   }
@@ -436,7 +430,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         uint32_t t[kOutTerms];
-        split2(make_float2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1]), t);
+        split2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1], t);
         uint8_t* o2 = rec + row_piece(127 - 16 * (pi + pj) - r4 - 8 * (z & 1), 8 * (z >> 1) + j2) + pair_base(pj);
         *reinterpret_cast<uint32_t*>(o2 + term_base(0)) = t[0];
         *reinterpret_cast<uint32_t*>(o2 + term_base(1)) = t[1];

@@ -49,7 +49,7 @@ constexpr uint32_t kOutAt = kScanStages * kStageBytes;  // o rows on their way o
 struct ScanCtl {
   uint64_t full[kScanStages], empty[kScanStages];
   uint64_t s_ready[2], d3[2];
-  uint64_t r_ready, u_ready, d1, d2, o_ready, o_free, drain;
+  uint64_t r_ready, u_ready, d1, d2, d2o, o_ready, o_free, drain;
   uint32_t tmem;
   int32_t abort;
 };
@@ -141,7 +141,7 @@ __device__ __forceinline__ void put_terms(const float (&x)[16], uint32_t hi, uin
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t w[kTerms];
-    split3(make_float2(x[2 * i], x[2 * i + 1]), w);
+    split3(x[2 * i], x[2 * i + 1], w);
 #pragma unroll
     for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
   }
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     sqk::mbar_init(&ctl.o_free, 1);
     sqk::mbar_init(&ctl.d1, 1);
     sqk::mbar_init(&ctl.d2, 1);
+    sqk::mbar_init(&ctl.d2o, 1);
     sqk::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     sqk::fence_mbar_init();
@@ -322,22 +323,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                    mma_desc(64, false), s < 1 || ks > 0);
       }
       __syncwarp();
-      // rows 16 kk .. 63 of T and P T see columns 16 kk .. 16 kk + 15. Terms of r and of T: the six largest products
-      // for T, the largest last; P T joins three of them, the first of which sets the accumulators
+      // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15: the six largest products of terms of r and of T, the
+      // largest last; then the three largest for P T
       if (!warp_wait(ctl, &ctl.r_ready, ph, ns)) break;
       tc_after();
       if (elect_one()) {
         const uint64_t prep = smem_desc(stage + kStagePrep, 128, 256, 0);
-        constexpr int pr[6] = {1, 2, 0, 1, 0, 0}, pt[6] = {0, 0, 2, 1, 1, 0};
+        constexpr int pr[6] = {2, 0, 1, 1, 0, 0}, pt[6] = {0, 2, 1, 0, 1, 0};
 #pragma unroll
         for (int x = 0; x < 6; ++x)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t b = prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16;
-            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk, b,
-                   mma_desc(x >= 1 && x <= 3 ? 64 - 16 * kk : 128 - 32 * kk, false), x > 0 || kk > 0);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk,
+                   prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16,
+                   mma_desc(64 - 16 * kk, false), x > 0 || kk > 0);
         tc_commit(&ctl.d2);
+#pragma unroll
+        for (int x = 3; x < 6; ++x)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // P T follows T's 64 - 16 kk rows, 32 bytes each
+            tc_mma(tm + TM_D2 + 64, tm + TM_RU + 32 * pr[x] + 8 * kk,
+                   prep + (term_base(pt[x]) + pair_base(kk) + 32 * (64 - 16 * kk)) / 16, mma_desc(64 - 16 * kk, false),
+                   x > 3 || kk > 0);
+        tc_commit(&ctl.d2o);
       }
       __syncwarp();
       if (!warp_wait(ctl, &ctl.u_ready, ph, ns)) break;
@@ -371,32 +379,38 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const uint32_t ru = tl + TM_RU + 8 * part;  // r and u of rows 16 part .. + 15
     put_state(0);
     put_state(1);
-    for (int i = 0; i < blocks; ++i) {
-      const int sg = i & 1;
-      const uint32_t ph = i & 1;
-      uint8_t* stage = smem + sg * kStageBytes;
-      if (!warp_wait(ctl, &ctl.full[sg], (i >> 1) & 1, ns)) break;
-      const int live = min(64, n - 64 * i), mine = live - 16 * part;  // rows; of this thread
+    float x[16];
+    // block i's rows: beta v into x; false where the wait ran out
+    auto take_rows = [&](int i) {
+      if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns)) return false;
+      uint8_t* stage = smem + (i & 1) * kStageBytes;
+      const int live = n - 64 * i;
       if (live < 64) {
         // rows of the k tile behind the request's last: another request's, or none's
-        for (int x = tid; x < (64 - live) * 16; x += kScanCompute)
-          *reinterpret_cast<uint4*>(stage + kTileBytes / 2 + ((x >> 3) & 1) * kTileBytes + (live + (x >> 4)) * 128 +
-                                    (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+        for (int y = tid; y < (64 - live) * 16; y += kScanCompute)
+          *reinterpret_cast<uint4*>(stage + kTileBytes / 2 + ((y >> 3) & 1) * kTileBytes + (live + (y >> 4)) * 128 +
+                                    (y & 7) * 16) = make_uint4(0, 0, 0, 0);
         sqk::fence_proxy_async_smem();
       }
       const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 16 * part * 128 + col;
-      const float* coef = reinterpret_cast<const float*>(stage + kStagePrep + kTermsBytes);
-      const float4* eg = reinterpret_cast<const float4*>(coef + 16 * part);  // e^G; 16 float4s on: beta, beta e^G, e^(G63 - G)
-      float x[16];
-      uint32_t w[16];
+      const float4* eb = reinterpret_cast<const float4*>(stage + kStagePrep + kTermsBytes) + 16 + 4 * part;
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
-        const float4 e = eg[16 + (j >> 2)];
+        const float4 e = eb[j >> 2];
         x[j] = e.x * __bfloat162float(v[j * 128]);
         x[j + 1] = e.y * __bfloat162float(v[(j + 1) * 128]);
         x[j + 2] = e.z * __bfloat162float(v[(j + 2) * 128]);
         x[j + 3] = e.w * __bfloat162float(v[(j + 3) * 128]);
       }
+      return true;
+    };
+    bool ok = take_rows(0);
+    for (int i = 0; i < blocks && ok; ++i) {
+      const uint32_t ph = i & 1;
+      const int live = min(64, n - 64 * i), mine = live - 16 * part;  // rows; of this thread
+      const float* coef = reinterpret_cast<const float*>(smem + (i & 1) * kStageBytes + kStagePrep + kTermsBytes);
+      const float4* eg = reinterpret_cast<const float4*>(coef + 16 * part);  // e^G; 16 float4s on: beta, beta e^G, e^(G63 - G)
+      uint32_t w[16];
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
       tc_ld16(w, tl + TM_D1K + 16 * part);
@@ -428,66 +442,60 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         x[j + 2] = e.z * __uint_as_float(w[j + 2]);
         x[j + 3] = e.w * __uint_as_float(w[j + 3]);
       }
+      // u's terms take r's place when the P T products have read it
+      if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
       put_terms(x, ru, ru + 32, ru + 64);
       warp_arrive(&ctl.u_ready);
 
-      // o, under the state's product
-      uint32_t o2[8];
-      float bad = 0.0f;  // stays 0 while every o is finite
+      // under the state's product: o on its way out, the next block's rows in
+      if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
       {
         uint32_t y[16];
+        tc_after();
         tc_ld16(w, tl + TM_D1Q + 16 * part);
         tc_ld16(y, tl + TM_D2 + 112 - 16 * part);
         tc_wait_ld(w);
         tc_wait_ld(y);
+        uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 16 * part * 128 + col;
+        float bad = 0.0f;  // stays 0 while every o is finite
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 e = eg[j >> 2];
-          const float p0 = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[15 - j]));
-          const float p1 = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[14 - j]));
-          const float p2 = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[13 - j]));
-          const float p3 = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[12 - j]));
-          bad = fmaf(p0, 0.0f, fmaf(p1, 0.0f, fmaf(p2, 0.0f, fmaf(p3, 0.0f, bad))));
-          o2[j >> 1] = bf16x2(p0, p1);
-          o2[(j >> 1) + 1] = bf16x2(p2, p3);
+          x[j] = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[15 - j]));
+          x[j + 1] = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[14 - j]));
+          x[j + 2] = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[13 - j]));
+          x[j + 3] = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[12 - j]));
+#pragma unroll
+          for (int z = j; z < j + 4; z += 2) {
+            bad = fmaf(x[z], 0.0f, fmaf(x[z + 1], 0.0f, bad));
+            const uint32_t t = bf16x2(x[z], x[z + 1]);
+            op[z * 128] = (uint16_t)t;
+            op[(z + 1) * 128] = (uint16_t)(t >> 16);
+          }
+        }
+        if (bad != 0.0f) {  // an infinity or a NaN: a NaN in a live row is reported
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < mine && x[j] != x[j]) st |= ST_NAN;
         }
       }
+      sqk::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
       const float g63 = coef[256];
-      bool ok = true;
+      if (i + 1 < blocks) ok = take_rows(i + 1);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         ok = ok && warp_wait(ctl, &ctl.d3[y], ph, ns);
         if (!ok) break;
         tc_after();
-        if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[sg]);  // this warp's reads of the stage came before
+        if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[i & 1]);  // this warp's reads of the stage came before
         tc_ld16(w, tl + TM_S + 64 * y + 16 * part);
         tc_wait_ld(w);
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 t = __ffma2_rn(make_float2(g63, g63), make_float2(S[y][j], S[y][j + 1]),
-                                      make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])));
-          S[y][j] = t.x;
-          S[y][j + 1] = t.y;
-        }
+        for (int j = 0; j < 16; ++j) S[y][j] = fmaf(g63, S[y][j], __uint_as_float(w[j]));
         if (i + 1 < blocks) put_state(y);
       }
-      if (!ok) break;
-      // o's rows go out while the next block's first product runs
-      if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
-      uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 16 * part * 128 + col;
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        op[j * 128] = (uint16_t)o2[j >> 1];
-        op[(j + 1) * 128] = (uint16_t)(o2[j >> 1] >> 16);
-      }
-      if (bad != 0.0f) {  // an infinity or a NaN: a NaN in a live row is reported
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < mine && ((o2[j >> 1] >> (16 * (j & 1))) & 0x7fffu) > 0x7f80u) st |= ST_NAN;
-      }
-      sqk::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
     }
   }
   tc_before();
