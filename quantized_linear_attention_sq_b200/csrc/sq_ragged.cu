@@ -2,6 +2,7 @@
 // include/sq_ragged.h: argument checks, launch rules and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -42,6 +43,22 @@ sq_status check_rows_of(const char* name, const void* p, int64_t stride, int64_t
   return SQ_OK;
 }
 
+// Allows a kernel all the shared memory of a CTA, once per device (`seen`: a
+// bit for each device that has it).
+template <typename K>
+cudaError_t allow_smem(K kernel, int device, std::atomic<uint64_t>& seen) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (seen.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  int optin = 0;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // ------------------------------------------------------------------- norms
 template <int D, typename TI, typename TO>
 void launch_norm(const sqr::NormArgs& a, int grid, cudaStream_t st) {
@@ -61,34 +78,42 @@ void launch_norm_from(int in, int out, const sqr::NormArgs& a, int grid, cudaStr
 }
 
 // --------------------------------------------------------------- recurrent
+struct RowsLaunch {
+  int device;
+  uint32_t max_rec;  // largest record, packed pools
+  cudaStream_t st;
+};
 template <int D, bool KDA, bool PACKED, typename T>
-cudaError_t launch_rows(const sqr::RaggedArgs& a, uint32_t max_rec, cudaStream_t st) {
+cudaError_t launch_rows(const sqr::RaggedArgs& a, const RowsLaunch& l) {
+  static std::atomic<uint64_t> seen{0};
   auto kern = sqr::k_ragged_rows<D, KDA, PACKED, T>;
-  const size_t smem = PACKED ? sqr::RGeo<D>::packed_smem(max_rec) : sqr::RGeo<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(kern, l.device, seen);
   if (e != cudaSuccess) return e;
-  kern<<<a.B * a.h_v, sqr::RGeo<D>::NT, smem, st>>>(a);
+  const size_t smem = PACKED ? sqr::RGeo<D>::packed_smem(l.max_rec) : sqr::RGeo<D>::SMEM;
+  kern<<<a.B * a.h_v, sqr::RGeo<D>::NT, smem, l.st>>>(a);
   return cudaGetLastError();
 }
 template <int D, bool KDA, typename T>
-cudaError_t launch_rows_pool(const sqr::RaggedArgs& a, uint32_t max_rec, cudaStream_t st) {
-  return a.fmt_fp32 ? launch_rows<D, KDA, false, T>(a, max_rec, st) : launch_rows<D, KDA, true, T>(a, max_rec, st);
+cudaError_t launch_rows_pool(const sqr::RaggedArgs& a, const RowsLaunch& l) {
+  return a.fmt_fp32 ? launch_rows<D, KDA, false, T>(a, l) : launch_rows<D, KDA, true, T>(a, l);
 }
 template <int D, bool KDA>
-cudaError_t launch_rows_type(int dtype, const sqr::RaggedArgs& a, uint32_t max_rec, cudaStream_t st) {
-  if (dtype == SQ_F32) return launch_rows_pool<D, KDA, float>(a, max_rec, st);
-  if (dtype == SQ_BF16) return launch_rows_pool<D, KDA, __nv_bfloat16>(a, max_rec, st);
-  return launch_rows_pool<D, KDA, __half>(a, max_rec, st);
+cudaError_t launch_rows_type(int dtype, const sqr::RaggedArgs& a, const RowsLaunch& l) {
+  if (dtype == SQ_F32) return launch_rows_pool<D, KDA, float>(a, l);
+  if (dtype == SQ_BF16) return launch_rows_pool<D, KDA, __nv_bfloat16>(a, l);
+  return launch_rows_pool<D, KDA, __half>(a, l);
 }
 template <int D>
-cudaError_t launch_rows_gate(bool kda, int dtype, const sqr::RaggedArgs& a, uint32_t max_rec, cudaStream_t st) {
-  return kda ? launch_rows_type<D, true>(dtype, a, max_rec, st) : launch_rows_type<D, false>(dtype, a, max_rec, st);
+cudaError_t launch_rows_gate(bool kda, int dtype, const sqr::RaggedArgs& a, const RowsLaunch& l) {
+  return kda ? launch_rows_type<D, true>(dtype, a, l) : launch_rows_type<D, false>(dtype, a, l);
 }
 
 // ------------------------------------------------------------------ blocks
 // Requests of at least this many rows run in blocks on the tensor cores,
-// shorter ones row by row.
-constexpr int kMinLong = 24;
+// shorter ones row by row. Measured on 48 requests of 1..420 rows into 8-bit
+// states and on 24 of 0..1900 (all kernels, us): from 6 rows 215, 257; from
+// 10 rows 215, 255; from 16 rows 217, 275; from 24 rows 227, 282.
+constexpr int kMinLong = 10;
 
 bool in_blocks(const sq_handle* h, int dtype, int32_t max_len) {
   return dtype == SQ_BF16 && h->desc.gate == SQ_GATE_HEAD && h->d == 128 && max_len >= kMinLong;
@@ -139,11 +164,10 @@ sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_r
   if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (s == SQ_OK) s = row_map(&om, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (s != SQ_OK) return s;
-  cudaError_t e = cudaFuncSetAttribute(sqr::k_chunk_prepare, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(sqr::PrepSmem));
+  static std::atomic<uint64_t> seen_prepare{0}, seen_fp32{0}, seen_packed{0};
   auto scan = r.fmt_fp32 ? sqr::k_chunk_scan<false> : sqr::k_chunk_scan<true>;
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sqr::kScanSmem);
+  cudaError_t e = allow_smem(sqr::k_chunk_prepare, h->device, seen_prepare);
+  if (e == cudaSuccess) e = allow_smem(scan, h->device, r.fmt_fp32 ? seen_fp32 : seen_packed);
   if (e != cudaSuccess) return cuda_fail(e, "setting the block kernels' shared memory");
   sqr::k_chunk_prepare<<<(unsigned)a.p.n_blocks * r.h_k, sqr::kPrepThreads, sizeof(sqr::PrepSmem), st>>>(a.p);
   e = cudaGetLastError();
@@ -249,7 +273,9 @@ sq_status sq_qk_norm(const sq_norm_desc* desc, const void* q, const void* k, int
   int per = sqr::kNormMaxRows;
   while (per > 1 && (rows + per - 1) / per < 2 * 148) per >>= 1;
   a.rows_per_cta = per;
-  const int grid = (rows + per - 1) / per;
+  const int slots = sqr::kNormThreads * 8 / d;
+  while ((1 << a.head_bits) < slots && (1 << a.head_bits) < h_q + h_k) a.head_bits++;
+  const int groups = (rows + per - 1) / per, grid = groups < 4 * 148 ? groups : 4 * 148;  // four CTAs per SM
   cudaStream_t st = as_stream(stream);
   if (d == 128) launch_norm_from<128>(in, out, a, grid, st);
   else if (d == 64) launch_norm_from<64>(in, out, a, grid, st);
@@ -320,7 +346,6 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   a.fmt_fp32 = h->desc.fmt == SQ_FMT_FP32;
   a.slot_bytes = h->slot_bytes;
   a.t = h->tables;
-  const uint32_t max_rec = a.fmt_fp32 ? 0u : (uint32_t)h->max_rec;
   cudaStream_t st = as_stream(stream);
   if (rows > 0 && in_blocks(h, dtype, max_len)) {
     if (((int64_t)rows / SQ_RAGGED_BLOCK + B) * h->desc.h_k > (int64_t)INT32_MAX)
@@ -330,9 +355,10 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
     if (s != SQ_OK) return s;
     h->launches += 2;
   }
-  if (d == 128) e = launch_rows_gate<128>(kda, dtype, a, max_rec, st);
-  else if (d == 64) e = launch_rows_gate<64>(kda, dtype, a, max_rec, st);
-  else e = launch_rows_gate<32>(kda, dtype, a, max_rec, st);
+  const RowsLaunch l{h->device, a.fmt_fp32 ? 0u : (uint32_t)h->max_rec, st};
+  if (d == 128) e = launch_rows_gate<128>(kda, dtype, a, l);
+  else if (d == 64) e = launch_rows_gate<64>(kda, dtype, a, l);
+  else e = launch_rows_gate<32>(kda, dtype, a, l);
   if (e != cudaSuccess) return cuda_fail(e, "launching the ragged rows");
   h->launches++;
   return SQ_OK;

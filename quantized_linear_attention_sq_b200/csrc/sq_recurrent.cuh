@@ -62,6 +62,16 @@ __device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(__half* p, float x) { *p = __float2half_rn(x); }
 
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__half* p, float4 x) {
+  const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 template <int D>
 struct RGeo {
   static constexpr int NT = 2 * D;              // threads
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   const bool resume = a.past && a.past[b] > 0;
   if (n == 0 && resume) return;
   const int c4 = 4 * (lane % R::LPR), rsub = lane / R::LPR;
-  const int row0 = warp * R::RP * R::RPT + rsub;  // this thread's key rows: row0 + r RP
+  const int row0 = (warp * R::RP + rsub) * R::RPT;  // this thread's key rows: RPT from there
   uint8_t* record = a.pool + (uint64_t)slot * a.slot_bytes + (PACKED ? a.t.rec_off[h] : 0u);
   float* S_pool = reinterpret_cast<float*>(a.pool) + ((size_t)slot * a.h_v + h) * D * D;
 
@@ -203,11 +213,11 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   if (PACKED && resume) {
     unpack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) S[r] = *reinterpret_cast<const float4*>(Ssh + (row0 + r * R::RP) * D + c4);
+    for (int r = 0; r < R::RPT; ++r) S[r] = *reinterpret_cast<const float4*>(Ssh + (row0 + r) * D + c4);
   } else {
 #pragma unroll
     for (int r = 0; r < R::RPT; ++r)
-      S[r] = resume ? *reinterpret_cast<const float4*>(S_pool + (size_t)(row0 + r * R::RP) * D + c4)
+      S[r] = resume ? *reinterpret_cast<const float4*>(S_pool + (size_t)(row0 + r) * D + c4)
                     : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   if (n > 0) deposit(vec);
@@ -223,14 +233,19 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
     const float gate = KDA ? 1.0f : w[4 * D + 1];
     float4 p = make_float4(0.f, 0.f, 0.f, 0.f), s = p;
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) {
-      const int i = row0 + r * R::RP;
-      const float ki = w[i], qi = w[D + i], gi = KDA ? w[3 * D + i] : gate;
-      S[r].x *= gi; S[r].y *= gi; S[r].z *= gi; S[r].w *= gi;
-      p.x = fmaf(S[r].x, ki, p.x); p.y = fmaf(S[r].y, ki, p.y);
-      p.z = fmaf(S[r].z, ki, p.z); p.w = fmaf(S[r].w, ki, p.w);
-      s.x = fmaf(S[r].x, qi, s.x); s.y = fmaf(S[r].y, qi, s.y);
-      s.z = fmaf(S[r].z, qi, s.z); s.w = fmaf(S[r].w, qi, s.w);
+    for (int r4 = 0; r4 < R::RPT; r4 += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(w + row0 + r4), q4 = *reinterpret_cast<const float4*>(w + D + row0 + r4);
+      const float4 g4 = KDA ? *reinterpret_cast<const float4*>(w + 3 * D + row0 + r4) : make_float4(gate, gate, gate, gate);
+      const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w}, gg[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int r = r4 + y;
+        S[r].x *= gg[y]; S[r].y *= gg[y]; S[r].z *= gg[y]; S[r].w *= gg[y];
+        p.x = fmaf(S[r].x, kk[y], p.x); p.y = fmaf(S[r].y, kk[y], p.y);
+        p.z = fmaf(S[r].z, kk[y], p.z); p.w = fmaf(S[r].w, kk[y], p.w);
+        s.x = fmaf(S[r].x, qq[y], s.x); s.y = fmaf(S[r].y, qq[y], s.y);
+        s.z = fmaf(S[r].z, qq[y], s.z); s.w = fmaf(S[r].w, qq[y], s.w);
+      }
     }
 #pragma unroll
     for (int d = R::LPR; d < 32; d <<= 1) {  // the key rows a warp covers at once
@@ -272,25 +287,30 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
       if (O.x != O.x || O.y != O.y || O.z != O.z || O.w != O.w) st |= ST_NAN;
       if (rsub == 0) {
         T* op = out + t * out_step + c4;
-        from_f32(op, O.x); from_f32(op + 1, O.y); from_f32(op + 2, O.z); from_f32(op + 3, O.w);
+        store4(op, O);
       }
     }
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) {
-      const float ki = w[row0 + r * R::RP];
-      S[r].x = fmaf(ki, u.x, S[r].x); S[r].y = fmaf(ki, u.y, S[r].y);
-      S[r].z = fmaf(ki, u.z, S[r].z); S[r].w = fmaf(ki, u.w, S[r].w);
+    for (int r4 = 0; r4 < R::RPT; r4 += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(w + row0 + r4);
+      const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float4& t = S[r4 + y];
+        t.x = fmaf(kk[y], u.x, t.x); t.y = fmaf(kk[y], u.y, t.y);
+        t.z = fmaf(kk[y], u.z, t.z); t.w = fmaf(kk[y], u.w, t.w);
+      }
     }
     cur = nxt;
   }
 
   if (PACKED) {
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r * R::RP) * D + c4) = S[r];
+    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r) * D + c4) = S[r];
     st |= pack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });  // its first barrier orders S
   } else {
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(S_pool + (size_t)(row0 + r * R::RP) * D + c4) = S[r];
+    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(S_pool + (size_t)(row0 + r) * D + c4) = S[r];
   }
   if (st) atomicOr(a.t.status, st);
 }

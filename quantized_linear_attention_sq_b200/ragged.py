@@ -13,19 +13,31 @@ from dataclasses import dataclass
 import torch
 
 from . import _abi
-from .state import DTYPES, _ptr, _stream, row_ptr
+from .state import DTYPES, _raw_stream, row_ptr
 
 BLOCK = _abi.SQ_RAGGED_BLOCK
+I32, U8, F32 = torch.int32, torch.uint8, torch.float32
 
 
-def _same_device(*ts):
-    ts = [t for t in ts if t is not None]
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if t.device != ts[0].device:
-            raise ValueError(f"tensors on {ts[0].device} and {t.device}")
-    return ts[0].device
+def _arg(t, dtype, name, numel, dev):
+    """Address of a contiguous tensor on CUDA device `dev` (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_cuda and t.get_device() == dev and t.is_contiguous() and numel in (None, t.numel()):
+        return t.data_ptr()
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, not on {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids=None, slot_used=None,
@@ -35,23 +47,23 @@ def batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slo
     positions int32 [max_rows], block_req int32 [max_rows // 64 + B] or more.
     slot_ids, slot_out int32 [B] and slot_used, used_out uint8 [n_slots]: all
     four or none; requests with slot_ids < 0 take free slots."""
+    dev = _device_of(lengths, "lengths")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids, slot_used,
+                                slot_out, used_out, status, stream)
     B, rows = lengths.numel(), positions.numel()
-    i32 = torch.int32
-    dev = _same_device(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids, slot_used, slot_out,
-                       used_out, status)
     if block_req.numel() < rows // BLOCK + B:
         raise ValueError(f"block_req has {block_req.numel()} elements, {rows // BLOCK + B} are needed")
-    slots = [slot_ids, slot_used, slot_out, used_out]
-    if any(t is None for t in slots) and not all(t is None for t in slots):
+    if not (slot_ids is None) == (slot_used is None) == (slot_out is None) == (used_out is None):
         raise ValueError("slot_ids, slot_used, slot_out and used_out go together")
     n_slots = 0 if slot_used is None else slot_used.numel()
-    with torch.cuda.device(dev):
-        _abi.sq_batch_tables(_ptr(lengths, i32, "lengths"), _ptr(past, i32, "past", B), B, rows,
-                             _ptr(cu_seqlens, i32, "cu_seqlens", B + 1), _ptr(cu_blocks, i32, "cu_blocks", B + 1),
-                             _ptr(positions, i32, "positions"), _ptr(block_req, i32, "block_req"),
-                             _ptr(slot_ids, i32, "slot_ids", B), _ptr(slot_used, torch.uint8, "slot_used"), n_slots,
-                             _ptr(slot_out, i32, "slot_out", B), _ptr(used_out, torch.uint8, "used_out", n_slots),
-                             _ptr(status, i32, "status", 1), _stream(stream))
+    _abi.sq_batch_tables(_arg(lengths, I32, "lengths", None, dev), _arg(past, I32, "past", B, dev), B, rows,
+                         _arg(cu_seqlens, I32, "cu_seqlens", B + 1, dev), _arg(cu_blocks, I32, "cu_blocks", B + 1, dev),
+                         _arg(positions, I32, "positions", None, dev), _arg(block_req, I32, "block_req", None, dev),
+                         _arg(slot_ids, I32, "slot_ids", B, dev), _arg(slot_used, U8, "slot_used", None, dev), n_slots,
+                         _arg(slot_out, I32, "slot_out", B, dev), _arg(used_out, U8, "used_out", n_slots, dev),
+                         _arg(status, I32, "status", 1, dev), _raw_stream(stream, dev))
 
 
 @dataclass
@@ -97,16 +109,19 @@ def qk_norm(q, k, q_out, k_out, mode="l2", eps=1e-6, q_weight=None, k_weight=Non
     for t, name in ((q, "q"), (q_out, "q_out")):
         if t.dtype not in DTYPES:
             raise ValueError(f"{name} must be one of {tuple(DTYPES)}, got {t.dtype}")
-    dev = _same_device(q, k, q_out, k_out, q_weight, k_weight, positions, n_rows)
+    dev = _device_of(q, "q")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return qk_norm(q, k, q_out, k_out, mode, eps, q_weight, k_weight, q_scale, positions, rot_dim, base,
+                           interleaved, n_rows, stream)
     rows, hq, d = q.shape
     hk = k.shape[1]
-    desc = _abi.NormDesc(_abi.SQ_NORM_L2 if mode == "l2" else _abi.SQ_NORM_RMS, float(eps), float(q_scale),
-                         int(rot_dim), int(bool(interleaved)), float(base))
-    with torch.cuda.device(dev):
-        qp, qs = row_ptr(q, q.dtype, "q", (rows, hq, d), dev)
-        kp, ks = row_ptr(k, q.dtype, "k", (rows, hk, d), dev)
-        f32, i32 = torch.float32, torch.int32
-        _abi.sq_qk_norm(desc, qp, kp, qs, ks, DTYPES[q.dtype], _ptr(q_weight, f32, "q_weight", d),
-                        _ptr(k_weight, f32, "k_weight", d), _ptr(positions, i32, "positions", rows),
-                        _ptr(q_out, q_out.dtype, "q_out", rows * hq * d), _ptr(k_out, q_out.dtype, "k_out", rows * hk * d),
-                        DTYPES[q_out.dtype], rows, _ptr(n_rows, i32, "n_rows", 1), hq, hk, d, _stream(stream))
+    desc = _abi.NormDesc(_abi.SQ_NORM_L2 if mode == "l2" else _abi.SQ_NORM_RMS, eps, q_scale, rot_dim,
+                         1 if interleaved else 0, base)
+    tin, tout = q.dtype, q_out.dtype
+    qp, qs = row_ptr(q, tin, "q", rows, hq, d, dev)
+    kp, ks = row_ptr(k, tin, "k", rows, hk, d, dev)
+    _abi.sq_qk_norm(desc, qp, kp, qs, ks, DTYPES[tin], _arg(q_weight, F32, "q_weight", d, dev),
+                    _arg(k_weight, F32, "k_weight", d, dev), _arg(positions, I32, "positions", rows, dev),
+                    _arg(q_out, tout, "q_out", rows * hq * d, dev), _arg(k_out, tout, "k_out", rows * hk * d, dev),
+                    DTYPES[tout], rows, _arg(n_rows, I32, "n_rows", 1, dev), hq, hk, d, _raw_stream(stream, dev))

@@ -54,19 +54,29 @@ def _host_ptr(t: torch.Tensor | None, dtype, name, numel) -> int | None:
 DTYPES = {torch.float32: _abi.SQ_F32, torch.bfloat16: _abi.SQ_BF16, torch.float16: _abi.SQ_F16}
 
 
-def row_ptr(t: torch.Tensor, dtype, name, shape, device):
+def _raw_stream(stream, dev: int) -> int:
+    """Address of a stream, or of device `dev`'s current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def row_ptr(t: torch.Tensor, dtype, name, rows, heads, d, dev: int):
     """(address, row stride in elements) of a [rows, heads, d] tensor whose
     rows may lie apart (a column slice of a wider matrix)."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    shape, st = t.shape, t.stride()
+    if (t.dtype is dtype and t.is_cuda and t.get_device() == dev and len(shape) == 3 and shape[0] == rows
+            and shape[1] == heads and shape[2] == d and st[2] == 1 and (st[1] == d or heads == 1)):
+        return t.data_ptr(), st[0] if rows > 1 else heads * d
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, not on {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    rows, heads, d = shape
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    if tuple(shape) != (rows, heads, d):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, heads, d)}")
+    if t.numel():
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 else heads * d
+    return t.data_ptr(), heads * d
 
 
 class StatePool:
@@ -222,24 +232,28 @@ class StatePool:
             raise ValueError("cu_blocks or block_req is too short for the batch")
         gn = rows * hv * (d if self.gate_kind == _abi.SQ_GATE_KEY_CHANNEL else 1)
         max_len = rows if max_len is None else int(max_len)
-        need = self.ragged_workspace_bytes(B, rows, max_len, q.dtype)
-        with torch.cuda.device(self.device):
-            if workspace is None and need:
+        dev = self.device.index
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.prefill_ragged(pool, q, k, v, beta, g, o, tables, slot_ids, max_len, workspace, stream)
+        if workspace is None:
+            need = self.ragged_workspace_bytes(B, rows, max_len, q.dtype)
+            if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
                 if isinstance(stream, torch.cuda.Stream):
                     workspace.record_stream(stream)
-            i32 = torch.int32
-            t = _abi.RaggedTables(_ptr(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
-                                  _ptr(tables.cu_blocks, i32, "cu_blocks", B + 1),
-                                  _ptr(tables.block_req, i32, "block_req"), _ptr(tables.past, i32, "past", B))
-            qp, qs = row_ptr(q, q.dtype, "q", (rows, hk, d), self.device)
-            kp, ks = row_ptr(k, q.dtype, "k", (rows, hk, d), self.device)
-            vp, vs = row_ptr(v, q.dtype, "v", (rows, hv, d), self.device)
-            _abi.sq_prefill_ragged(self._h, self._check_pool(pool), qp, kp, vp, qs, ks, vs, DTYPES[q.dtype],
-                                   _ptr(beta, torch.float32, "beta", rows * hv), _ptr(g, torch.float32, "g", gn),
-                                   _ptr(o, q.dtype, "o", rows * hv * d), t, _ptr(slot_ids, i32, "slot_ids", B), B,
-                                   rows, max_len, _ptr(workspace, torch.uint8, "workspace"),
-                                   workspace.numel() if workspace is not None else 0, _stream(stream))
+        i32 = torch.int32
+        t = _abi.RaggedTables(_ptr(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
+                              _ptr(tables.cu_blocks, i32, "cu_blocks", B + 1),
+                              _ptr(tables.block_req, i32, "block_req"), _ptr(tables.past, i32, "past", B))
+        qp, qs = row_ptr(q, q.dtype, "q", rows, hk, d, dev)
+        kp, ks = row_ptr(k, q.dtype, "k", rows, hk, d, dev)
+        vp, vs = row_ptr(v, q.dtype, "v", rows, hv, d, dev)
+        _abi.sq_prefill_ragged(self._h, self._check_pool(pool), qp, kp, vp, qs, ks, vs, DTYPES[q.dtype],
+                               _ptr(beta, torch.float32, "beta", rows * hv), _ptr(g, torch.float32, "g", gn),
+                               _ptr(o, q.dtype, "o", rows * hv * d), t, _ptr(slot_ids, i32, "slot_ids", B), B, rows,
+                               max_len, _ptr(workspace, torch.uint8, "workspace"),
+                               workspace.numel() if workspace is not None else 0, _raw_stream(stream, dev))
 
     def dequantize_state(self, pool, S_out, slot_ids=None, stream=None):
         B = S_out.shape[0]
