@@ -123,8 +123,8 @@ typedef struct {
  *            (all 16-byte aligned, row strides a multiple of 16 bytes)
  *   beta     device fp32 [rows, h_v]
  *   g        device fp32 [rows, h_v] (SQ_GATE_HEAD) or [rows, h_v, d]
- *            (SQ_GATE_KEY_CHANNEL), in [0, 1]; values outside are taken as
- *            the nearer bound
+ *            (SQ_GATE_KEY_CHANNEL, then 16-byte aligned), in [0, 1]; values
+ *            outside are taken as the nearer bound
  *   o        device, type `dtype`, contiguous [rows, h_v, d]; rows of no request are left as they were
  *   slot_ids device int32 [B] (distinct), or NULL for slots 0..B-1; a
  *            request whose slot is out of range gets o = 0 and

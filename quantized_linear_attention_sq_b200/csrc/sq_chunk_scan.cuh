@@ -57,7 +57,6 @@ constexpr size_t kScanSmem = 1024 + kOutAt + kTileBytes + sizeof(ScanCtl) + 16;
 
 struct ScanArgs {
   PrepArgs p;
-  uint64_t wait_ns;
 };
 
 // Columns of tensor memory (480 of 512).
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tm = ctl.tmem;
-  const uint64_t ns = args.wait_ns;
+  const uint64_t ns = a.wait_ns;
   uint32_t st = 0;
 
   if (warp == kMoveWarp) {  // ------------------------------------- loads and stores

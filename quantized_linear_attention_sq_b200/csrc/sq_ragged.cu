@@ -55,6 +55,8 @@ cudaError_t allow_smem(K kernel, int device, std::atomic<uint64_t>& seen) {
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - (int)fa.sharedSizeBytes);
+  // all of the unified storage as shared memory, so that as many CTAs fit as the kernel is laid out for
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_release);
   return e;
 }
@@ -79,8 +81,7 @@ void launch_norm_from(int in, int out, const sqr::NormArgs& a, int grid, cudaStr
 
 // --------------------------------------------------------------- recurrent
 struct RowsLaunch {
-  int device;
-  uint32_t max_rec;  // largest record, packed pools
+  int device, sms;
   cudaStream_t st;
 };
 template <int D, bool KDA, bool PACKED, typename T>
@@ -89,8 +90,9 @@ cudaError_t launch_rows(const sqr::RaggedArgs& a, const RowsLaunch& l) {
   auto kern = sqr::k_ragged_rows<D, KDA, PACKED, T>;
   const cudaError_t e = allow_smem(kern, l.device, seen);
   if (e != cudaSuccess) return e;
-  const size_t smem = PACKED ? sqr::RGeo<D>::packed_smem(l.max_rec) : sqr::RGeo<D>::SMEM;
-  kern<<<a.B * a.h_v, sqr::RGeo<D>::NT, smem, l.st>>>(a);
+  const size_t smem = sqr::RGeo<D>::smem(PACKED, a.rec_cap);
+  const int64_t tiles = (int64_t)a.B * a.h_v, most = 2ll * l.sms * (128 / D) * (128 / D);
+  kern<<<(int)(tiles < most ? tiles : most), sqr::RGeo<D>::NT, smem, l.st>>>(a);
   return cudaGetLastError();
 }
 template <int D, bool KDA, typename T>
@@ -157,7 +159,6 @@ sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_r
   a.p.block_req = t.block_req;
   a.p.ws = static_cast<uint8_t*>(workspace);
   a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
-  a.wait_ns = h->wait_ns;
   CUtensorMap qm, km, vm, om;
   sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -325,7 +326,7 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
     if (s == SQ_OK) s = check_rows_of("v", v, v_row_stride, (int64_t)h->desc.h_v * d, eb, rows);
     if (s != SQ_OK) return s;
     SQ_NEED(beta, 4);
-    SQ_NEED(g, 4);
+    SQ_NEED(g, kda ? 16 : 4);
     SQ_NEED(o, 16);
   }
   if (workspace_bytes < need)
@@ -344,7 +345,9 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   a.cu_seqlens = cu_seqlens; a.past = tables->past; a.slots = slot_ids;
   a.B = B; a.rows = rows; a.h_v = h->desc.h_v; a.h_k = h->desc.h_k; a.n_slots = h->desc.n_slots;
   a.fmt_fp32 = h->desc.fmt == SQ_FMT_FP32;
+  a.rec_cap = a.fmt_fp32 ? 0u : (uint32_t)h->max_rec;
   a.slot_bytes = h->slot_bytes;
+  a.wait_ns = h->wait_ns;
   a.t = h->tables;
   cudaStream_t st = as_stream(stream);
   if (rows > 0 && in_blocks(h, dtype, max_len)) {
@@ -355,7 +358,7 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
     if (s != SQ_OK) return s;
     h->launches += 2;
   }
-  const RowsLaunch l{h->device, a.fmt_fp32 ? 0u : (uint32_t)h->max_rec, st};
+  const RowsLaunch l{h->device, h->num_sms, st};
   if (d == 128) e = launch_rows_gate<128>(kda, dtype, a, l);
   else if (d == 64) e = launch_rows_gate<64>(kda, dtype, a, l);
   else e = launch_rows_gate<32>(kda, dtype, a, l);

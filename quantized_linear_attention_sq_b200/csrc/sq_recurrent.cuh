@@ -1,18 +1,20 @@
 // sq_recurrent.cuh -- the gated delta rule row by row over a ragged batch
 // (sq_prefill_ragged: single tokens, short requests, gates by key channel).
 //
-// One CTA of 2 D threads per (request, value head); the fp32 state stays in
-// registers from its load to its store: a lane owns four columns of RPT key
-// rows, so a warp reads and writes whole rows of the state with 16-byte
-// accesses. A row (token) costs one barrier: with S the gated state before
-// the update,
+// CTAs of 2 D threads, two per SM, walk over (request, value head) tiles; a
+// tile's fp32 state stays in registers from its load to its store: a lane
+// owns four columns of RPT key rows, so a warp reads and writes whole rows of
+// the state with 16-byte accesses. A row (token) costs one barrier: with S
+// the gated state before the update,
 //     p = S^T k,  u = beta (v - p),  o = (S + k u^T)^T q = S^T q + (k . q) u,
 // so both column sums are taken of the same state, their per-warp partials
 // cross the CTA through shared memory once, and every thread finishes the
 // sums of its own columns and applies S += k u^T.
-// One row per request is bound by HBM (the state is read and written once:
-// 2 x 64 KiB per head at D = 128, two CTAs per SM keep 128 KiB in flight);
-// many rows are bound by the latency of that exchange.
+// One row per request is bound by HBM (the state is read and written once, 2
+// x 64 KiB per head at D = 128): the next tile's state (or packed record)
+// comes into shared memory by bulk copy while this one is worked on, and its
+// first row's vectors are fetched before this one's state is stored. Many
+// rows are bound by the latency of the exchange.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,7 +43,8 @@ struct RaggedArgs {
   const int32_t* slots;       // [B] or null
   int32_t B, rows, h_v, h_k, n_slots, fmt_fp32;
   int32_t min_long;           // requests of at least this many rows are another kernel's (0: none is)
-  uint64_t slot_bytes;
+  uint32_t rec_cap;           // largest packed record
+  uint64_t slot_bytes, wait_ns;
   Tables t;
 };
 
@@ -51,8 +54,10 @@ __device__ __forceinline__ void ragged_span(const RaggedArgs& a, int b, int& fir
   n = min(max(a.cu_seqlens[b + 1], first), a.rows) - first;
 }
 
-__device__ __forceinline__ float clamp_gate(float g) {
-  return g != g ? g : fminf(fmaxf(g, 0.0f), 1.0f);  // a NaN stays one
+__device__ __forceinline__ float clamp_gate(float g) {  // to [0, 1]; a NaN stays one
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0f00000000;\n\tmin.NaN.f32 %0, t, 0f3F800000;\n\t}" : "=f"(r) : "f"(g));
+  return r;
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -72,6 +77,32 @@ __device__ __forceinline__ void store4(__half* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// Four elements as fp32.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const __half* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sqk::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// One row's vectors in shared memory, as they came: k, q, v, then (fp32) the
+// key channels' gates, beta, the head's gate.
+template <int D, typename T>
+struct RowVectors {
+  T k[D], q[D], v[D];
+  float g[D];
+  float beta, gate, pad[2];
+};
+
 template <int D>
 struct RGeo {
   static constexpr int NT = 2 * D;              // threads
@@ -79,28 +110,34 @@ struct RGeo {
   static constexpr int LPR = D / 4;             // lanes per key row (four columns each)
   static constexpr int RP = 32 / LPR;           // key rows a warp covers at once
   static constexpr int RPT = D / (NW * RP);     // key rows per thread
-  static constexpr int VEC = 4 * D + 4;         // floats of a row's vectors: k q v g | beta, gate
   static constexpr int RED = 2 * NW * D;        // floats of the warps' partials: p, o
-  static constexpr size_t FLOATS = 3 * VEC + 2 * RED;
-  static constexpr size_t SMEM = FLOATS * 4;
-  // packed pools: the fp32 state on its way between the record's thread map
-  // and this kernel's, the record, the head's row tables
-  static size_t packed_smem(uint32_t rec) { return SMEM + (size_t)D * D * 4 + (rec + 15) / 16 * 16 + 7 * D; }
+  static constexpr int RING = 4;                // rows' vectors at hand or on their way
+  static constexpr size_t FIXED = ((size_t)RING * sizeof(RowVectors<D, float>) + 2 * RED * 4 + 127) / 128 * 128;
+  static constexpr size_t STATE = (size_t)D * D * 4;
+  // fp32 pools: the next tile's state. Packed pools: the fp32 state on its way
+  // between the record's thread map and this kernel's, the next tile's
+  // record, the record going out with the head's row tables
+  static size_t smem(bool packed, uint32_t rec) {
+    const size_t r = (rec + 127) / 128 * 128;
+    return FIXED + STATE + (packed ? 2 * r + 7 * D : 0);
+  }
 };
 
-// The slot's packed record, dequantized into S [D][D] in shared memory.
+// A tile of work: rows `first` .. + n of one request, one value head.
+struct RowTile {
+  int32_t b, h, first, n, slot;
+  int32_t what;  // TILE_*
+};
+enum { TILE_END = 0, TILE_RUN = 1, TILE_RESUME = 2, TILE_ZERO = 4 };  // RUN: store a state; ZERO: a bad slot, o = 0
+
+// A packed record in shared memory, dequantized into S [D][D] there.
 // `sync`: a barrier of the Geo<D>::NT threads that call it.
 template <int D, typename Sync>
-__device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const uint8_t* src, uint8_t* rec, float* S,
-                                             Sync sync) {
+__device__ __forceinline__ void unpack_record(const RaggedArgs& a, int h, const uint8_t* rec, float* S, Sync sync) {
   using G = Geo<D>;
   static_assert(G::NT == RGeo<D>::NT, "one thread map");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cc = lane % G::LPR, rg = warp * G::RPW + lane / G::LPR;
-  const uint32_t rb = a.t.rec_bytes[h];
-  for (uint32_t x = tid * 16; x < rb; x += G::NT * 16)
-    *reinterpret_cast<uint4*>(rec + x) = *reinterpret_cast<const uint4*>(src + x);
-  sync();
   const float* col = a.t.col + (size_t)h * D + 16 * cc;
 #pragma unroll
   for (int r = 0; r < G::RPT; ++r) {
@@ -115,6 +152,16 @@ __device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const u
           __fmul2_rn(T[p], make_float2(col[2 * p], col[2 * p + 1]));
   }
   sync();
+}
+// The same from the pool, through `rec`.
+template <int D, typename Sync>
+__device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const uint8_t* src, uint8_t* rec, float* S,
+                                             Sync sync) {
+  const uint32_t rb = a.t.rec_bytes[h];
+  for (uint32_t x = threadIdx.x * 16; x < rb; x += Geo<D>::NT * 16)
+    *reinterpret_cast<uint4*>(rec + x) = *reinterpret_cast<const uint4*>(src + x);
+  sync();
+  unpack_record<D>(a, h, rec, S, sync);
 }
 
 // S [D][D] in shared memory, quantized into the slot's record
@@ -151,166 +198,264 @@ __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8
   return st;
 }
 
+// The search for a CTA's next tile of work, by one warp: each lane looks at
+// one of the next 32 tiles of the CTA. What it needs of them is on its way to
+// shared memory (`ask`) while the warp does other work, then `answer` picks
+// the first tile with work (asking again where none has any).
+struct TileSearch {
+  int32_t got[4][32];  // cu_seqlens[b], cu_seqlens[b + 1], past[b], slots[b]
+};
+__device__ __forceinline__ void ask(const RaggedArgs& a, TileSearch& s, uint32_t at, uint32_t step) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = at + lane * step;
+  if (mine >= at && mine < (uint32_t)a.B * a.h_v) {
+    const uint32_t b = mine / a.h_v;
+    sqk::cp_async4(&s.got[0][lane], a.cu_seqlens + b);
+    sqk::cp_async4(&s.got[1][lane], a.cu_seqlens + b + 1);
+    if (a.past) sqk::cp_async4(&s.got[2][lane], a.past + b);
+    if (a.slots) sqk::cp_async4(&s.got[3][lane], a.slots + b);
+  }
+  sqk::cp_async_commit();
+}
+__device__ __forceinline__ RowTile answer(const RaggedArgs& a, TileSearch& s, uint32_t& at, uint32_t step) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t tiles = (uint32_t)a.B * a.h_v;
+  while (at < tiles) {
+    sqk::cp_async_wait_all();
+    const uint32_t mine = at + lane * step;
+    RowTile t{};
+    if (mine >= at && mine < tiles) {
+      t.b = mine / a.h_v;
+      t.h = mine - t.b * a.h_v;
+      t.first = min(max(s.got[0][lane], 0), a.rows);
+      t.n = min(max(s.got[1][lane], t.first), a.rows) - t.first;
+      if (!(a.min_long && t.n >= a.min_long)) {
+        t.slot = a.slots ? s.got[3][lane] : t.b;
+        const bool resume = a.past && s.got[2][lane] > 0;
+        if (t.slot < 0 || t.slot >= a.n_slots) t.what = TILE_ZERO;
+        else if (t.n > 0 || !resume) t.what = resume ? TILE_RUN | TILE_RESUME : TILE_RUN;
+      }
+    }
+    const uint32_t found = __ballot_sync(0xffffffffu, t.what != TILE_END);
+    if (found) {
+      const int from = __ffs(found) - 1;
+      t.b = __shfl_sync(0xffffffffu, t.b, from);
+      t.h = __shfl_sync(0xffffffffu, t.h, from);
+      t.first = __shfl_sync(0xffffffffu, t.first, from);
+      t.n = __shfl_sync(0xffffffffu, t.n, from);
+      t.slot = __shfl_sync(0xffffffffu, t.slot, from);
+      t.what = __shfl_sync(0xffffffffu, t.what, from);
+      at += (from + 1) * step;
+      return t;
+    }
+    if (at + 32ull * step >= tiles) break;
+    at += 32 * step;
+    ask(a, s, at, step);
+  }
+  at = tiles;
+  return RowTile{};
+}
+
 template <int D, bool KDA, bool PACKED, typename T>
 __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs a) {
   using R = RGeo<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* vec = reinterpret_cast<float*>(smem);   // three rows' vectors
-  float* red = vec + 3 * R::VEC;                 // two rows' partials
-  float* Ssh = vec + R::FLOATS;                  // packed pools
-  uint8_t* rec = reinterpret_cast<uint8_t*>(Ssh + D * D);
-  const int b = blockIdx.x / a.h_v, h = blockIdx.x - b * a.h_v;
-  int first, n;
-  ragged_span(a, b, first, n);
-  if (a.min_long && n >= a.min_long) return;
+  using Row = RowVectors<D, T>;
+  Row* ring = reinterpret_cast<Row*>(smem);
+  float* red = reinterpret_cast<float*>(smem + R::RING * sizeof(RowVectors<D, float>));  // two rows' partials
+  float* Ssh = reinterpret_cast<float*>(smem + R::FIXED);  // fp32 pools: the incoming state; packed: see RGeo
+  uint8_t* rec_in = smem + R::FIXED + R::STATE;
+  __shared__ RowTile tiles[3];                   // this one, the next, the one behind it
+  __shared__ TileSearch search;
+  __shared__ __align__(8) uint64_t arrived;      // the incoming state or record
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slot = a.slots ? a.slots[b] : b;
-  T* out = static_cast<T*>(a.o) + ((size_t)first * a.h_v + h) * D;
-  const size_t out_step = (size_t)a.h_v * D;
-  if (slot < 0 || slot >= a.n_slots) {
-    for (int t = 0; t < n; ++t)
-      if (tid < D) from_f32(out + t * out_step + tid, 0.0f);
-    if (tid == 0) atomicOr(a.t.status, ST_SLOT);
-    return;
-  }
-  const bool resume = a.past && a.past[b] > 0;
-  if (n == 0 && resume) return;
   const int c4 = 4 * (lane % R::LPR), rsub = lane / R::LPR;
   const int row0 = (warp * R::RP + rsub) * R::RPT;  // this thread's key rows: RPT from there
-  uint8_t* record = a.pool + (uint64_t)slot * a.slot_bytes + (PACKED ? a.t.rec_off[h] : 0u);
-  float* S_pool = reinterpret_cast<float*>(a.pool) + ((size_t)slot * a.h_v + h) * D * D;
 
-  // thread tid < D brings k and v of channel tid, the others q and g
-  const int hk = h / (a.h_v / a.h_k);
-  const int ch = tid < D ? tid : tid - D;
-  float x0 = 0.0f, x1 = 0.0f, xb = 0.0f, xg = 1.0f;
-  auto fetch = [&](int t) {
-    const size_t row = (size_t)first + t;
-    if (tid < D) {
-      x0 = to_f32(static_cast<const T*>(a.k)[row * a.k_stride + hk * D + ch]);
-      x1 = to_f32(static_cast<const T*>(a.v)[row * a.v_stride + h * D + ch]);
-      if (tid == 0) xb = a.beta[row * a.h_v + h];
-      if (!KDA && tid == 1) xg = clamp_gate(a.g[row * a.h_v + h]);
-    } else {
-      x0 = to_f32(static_cast<const T*>(a.q)[row * a.q_stride + hk * D + ch]);
-      if (KDA) x1 = clamp_gate(a.g[(row * a.h_v + h) * D + ch]);
-    }
+  auto state_of = [&](const RowTile& t) { return reinterpret_cast<float*>(a.pool) + ((size_t)t.slot * a.h_v + t.h) * D * D; };
+  auto record_of = [&](const RowTile& t) { return a.pool + (uint64_t)t.slot * a.slot_bytes + a.t.rec_off[t.h]; };
+  auto bring = [&](const RowTile& t) {  // by one thread
+    if (!(t.what & TILE_RESUME)) return;
+    const uint32_t bytes = PACKED ? a.t.rec_bytes[t.h] : (uint32_t)R::STATE;
+    sqk::mbar_arrive_expect_tx(&arrived, bytes);
+    if (PACKED) sqk::bulk_g2s(rec_in, record_of(t), bytes, &arrived);
+    else sqk::bulk_g2s(Ssh, state_of(t), bytes, &arrived);
   };
-  auto deposit = [&](float* w) {
-    if (tid < D) {
-      w[ch] = x0;
-      w[2 * D + ch] = x1;
-      if (tid == 0) w[4 * D] = xb;
-      if (!KDA && tid == 1) w[4 * D + 1] = xg;
-    } else {
-      w[D + ch] = x0;
-      if (KDA) w[3 * D + ch] = x1;
-    }
-  };
-
-  float4 S[R::RPT];
-  if (n > 0) fetch(0);
-  if (PACKED && resume) {
-    unpack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });
-#pragma unroll
-    for (int r = 0; r < R::RPT; ++r) S[r] = *reinterpret_cast<const float4*>(Ssh + (row0 + r) * D + c4);
-  } else {
-#pragma unroll
-    for (int r = 0; r < R::RPT; ++r)
-      S[r] = resume ? *reinterpret_cast<const float4*>(S_pool + (size_t)(row0 + r) * D + c4)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (n > 0) deposit(vec);
-  __syncthreads();
-
-  uint32_t st = 0;
-  int cur = 0;  // t % 3
-  for (int t = 0; t < n; ++t) {
-    const float* w = vec + cur * R::VEC;
-    const int nxt = cur == 2 ? 0 : cur + 1;
-    float* rd = red + (t & 1) * R::RED;
-    if (t + 1 < n) fetch(t + 1);
-    const float gate = KDA ? 1.0f : w[4 * D + 1];
-    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), s = p;
-#pragma unroll
-    for (int r4 = 0; r4 < R::RPT; r4 += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(w + row0 + r4), q4 = *reinterpret_cast<const float4*>(w + D + row0 + r4);
-      const float4 g4 = KDA ? *reinterpret_cast<const float4*>(w + 3 * D + row0 + r4) : make_float4(gate, gate, gate, gate);
-      const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w}, gg[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int r = r4 + y;
-        S[r].x *= gg[y]; S[r].y *= gg[y]; S[r].z *= gg[y]; S[r].w *= gg[y];
-        p.x = fmaf(S[r].x, kk[y], p.x); p.y = fmaf(S[r].y, kk[y], p.y);
-        p.z = fmaf(S[r].z, kk[y], p.z); p.w = fmaf(S[r].w, kk[y], p.w);
-        s.x = fmaf(S[r].x, qq[y], s.x); s.y = fmaf(S[r].y, qq[y], s.y);
-        s.z = fmaf(S[r].z, qq[y], s.z); s.w = fmaf(S[r].w, qq[y], s.w);
+  // Row t of tile c on its way to a ring slot, one group of copies (an empty one if there is no such row).
+  auto fetch = [&](const RowTile& c, int t, uint32_t slot) {
+    if (t < c.n && (c.what & TILE_RUN)) {
+      Row& w = ring[slot % R::RING];
+      const size_t row = (size_t)c.first + t;
+      constexpr int P = D * (int)sizeof(T) / 16;  // pieces of 16 bytes of k, q and v
+      static_assert(3 * P + 2 <= R::NT && D / 4 + 2 <= R::NT, "one piece per thread");
+      const int hk = c.h / (a.h_v / a.h_k);
+      const int which = tid / P, x = tid % P * (16 / (int)sizeof(T));
+      if (which == 0) cp_async16(w.k + x, static_cast<const T*>(a.k) + row * a.k_stride + hk * D + x);
+      else if (which == 1) cp_async16(w.q + x, static_cast<const T*>(a.q) + row * a.q_stride + hk * D + x);
+      else if (which == 2) cp_async16(w.v + x, static_cast<const T*>(a.v) + row * a.v_stride + c.h * D + x);
+      else if (tid == 3 * P) sqk::cp_async4(&w.beta, a.beta + row * a.h_v + c.h);
+      else if (!KDA && tid == 3 * P + 1) sqk::cp_async4(&w.gate, a.g + row * a.h_v + c.h);
+      if (KDA && tid >= R::NT - D / 4) {
+        const int y = 4 * (tid - (R::NT - D / 4));
+        cp_async16(w.g + y, a.g + (row * a.h_v + c.h) * D + y);
       }
     }
+    sqk::cp_async_commit();
+  };
+
+  if (tid == 0) {
+    sqk::mbar_init(&arrived, 1);
+    sqk::fence_mbar_init();
+  }
+  uint32_t at = blockIdx.x;  // warp 0: the search goes on here
+  if (warp == 0) {
+    for (int x = 0; x < 2; ++x) {
+      ask(a, search, at, gridDim.x);
+      const RowTile t = answer(a, search, at, gridDim.x);
+      if (lane == 0) {
+        tiles[x] = t;
+        if (x == 0) bring(t);
+      }
+    }
+  }
+  __syncthreads();
+  uint32_t phase = 0, st = 0, base = 0;  // base: ring slot of the tile's first row
+  fetch(tiles[0], 0, 0);
+  fetch(tiles[0], 1, 1);
+  for (int turn = 0; tiles[turn].what != TILE_END; turn = turn == 2 ? 0 : turn + 1) {
+  const RowTile& c = tiles[turn];
+  const RowTile& nx = tiles[turn == 2 ? 0 : turn + 1];
+  const int n = c.n;
+  T* out = static_cast<T*>(a.o) + ((size_t)c.first * a.h_v + c.h) * D;
+  const size_t out_step = (size_t)a.h_v * D;
+  const bool resume = c.what & TILE_RESUME;
+  float4 S[R::RPT];
+  bool ok = true;
+  if (resume) {
+    ok = sqk::mbar_wait_bounded(&arrived, phase & 1, a.wait_ns);
+    ++phase;
+    if (PACKED && ok) unpack_record<D>(a, c.h, rec_in, Ssh, [] { __syncthreads(); });
+  }
 #pragma unroll
-    for (int d = R::LPR; d < 32; d <<= 1) {  // the key rows a warp covers at once
-      p.x += __shfl_xor_sync(0xffffffffu, p.x, d); p.y += __shfl_xor_sync(0xffffffffu, p.y, d);
-      p.z += __shfl_xor_sync(0xffffffffu, p.z, d); p.w += __shfl_xor_sync(0xffffffffu, p.w, d);
-      s.x += __shfl_xor_sync(0xffffffffu, s.x, d); s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
-      s.z += __shfl_xor_sync(0xffffffffu, s.z, d); s.w += __shfl_xor_sync(0xffffffffu, s.w, d);
+  for (int r = 0; r < R::RPT; ++r)
+    S[r] = resume && ok ? *reinterpret_cast<const float4*>(Ssh + (row0 + r) * D + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  cp_async_wait_but_one();  // the first row
+  if (!__syncthreads_and(ok)) {  // the state never came: the pool stays as it is
+    st |= sqk::ST_TIMEOUT;
+    break;
+  }
+  if (tid == 0) bring(nx);  // every thread has taken this tile's state
+  if (warp == 0) ask(a, search, at, gridDim.x);
+  if (c.what == TILE_ZERO) {
+    for (int t = 0; t < n; ++t)
+      if (tid < D) from_f32(out + t * out_step + tid, 0.0f);
+    st |= ST_SLOT;
+  }
+#pragma unroll 1
+  for (int t = 0; t < n && c.what != TILE_ZERO; ++t) {
+    const Row& w = ring[(base + t) % R::RING];
+    float* rd = red + (t & 1) * R::RED;
+    // the slot of row t + 2 was last read after the barrier of row t - 2, which every thread has left
+    fetch(c, t + 2, base + t + 2);
+    const float gate = KDA ? 1.0f : clamp_gate(w.gate);
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r4 = 0; r4 < R::RPT; r4 += 4) {
+      const float4 k4 = load4(w.k + row0 + r4);
+      float4 g4 = make_float4(gate, gate, gate, gate);
+      if (KDA) {
+        g4 = load4(w.g + row0 + r4);
+        g4 = make_float4(clamp_gate(g4.x), clamp_gate(g4.y), clamp_gate(g4.z), clamp_gate(g4.w));
+      }
+      const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, gg[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float4& x = S[r4 + y];
+        x.x *= gg[y]; x.y *= gg[y]; x.z *= gg[y]; x.w *= gg[y];
+        p.x = fmaf(x.x, kk[y], p.x); p.y = fmaf(x.y, kk[y], p.y);
+        p.z = fmaf(x.z, kk[y], p.z); p.w = fmaf(x.w, kk[y], p.w);
+      }
     }
-    if (rsub == 0) {
-      *reinterpret_cast<float4*>(rd + warp * D + c4) = p;
-      *reinterpret_cast<float4*>(rd + (R::NW + warp) * D + c4) = s;
+    auto deposit = [&](float4 x, float* to) {
+#pragma unroll
+      for (int d = R::LPR; d < 32; d <<= 1) {  // the key rows a warp covers at once
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, d); x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, d); x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
+      }
+      if (rsub == 0) *reinterpret_cast<float4*>(to + c4) = x;
+    };
+    deposit(p, rd + warp * D);
+    p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r4 = 0; r4 < R::RPT; r4 += 4) {
+      const float4 q4 = load4(w.q + row0 + r4);
+      const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float4& x = S[r4 + y];
+        p.x = fmaf(x.x, qq[y], p.x); p.y = fmaf(x.y, qq[y], p.y);
+        p.z = fmaf(x.z, qq[y], p.z); p.w = fmaf(x.w, qq[y], p.w);
+      }
     }
-    // slot nxt was last read after the barrier of row t - 2, which every
-    // thread has passed before the barrier of row t - 1
-    if (t + 1 < n) deposit(vec + nxt * R::VEC);
+    deposit(p, rd + (R::NW + warp) * D);
+    cp_async_wait_but_one();  // the next row
     __syncthreads();
-    float4 P = *reinterpret_cast<const float4*>(rd + c4);
+    auto collect = [&](const float* from) {
+      float4 x = *reinterpret_cast<const float4*>(from + c4);
 #pragma unroll
-    for (int x = 1; x < R::NW; ++x) {
-      const float4 y = *reinterpret_cast<const float4*>(rd + x * D + c4);
-      P.x += y.x; P.y += y.y; P.z += y.z; P.w += y.w;
-    }
-    const float beta = w[4 * D];
-    const float4 v = *reinterpret_cast<const float4*>(w + 2 * D + c4);
+      for (int y = 1; y < R::NW; ++y) {
+        const float4 z = *reinterpret_cast<const float4*>(from + y * D + c4);
+        x.x += z.x; x.y += z.y; x.z += z.z; x.w += z.w;
+      }
+      return x;
+    };
+    const float4 P = collect(rd), v = load4(w.v + c4);
+    const float beta = w.beta;
     const float4 u = make_float4(beta * (v.x - P.x), beta * (v.y - P.y), beta * (v.z - P.z), beta * (v.w - P.w));
     if (warp == t % R::NW) {  // the warps take turns at o
       float kq = 0.0f;
 #pragma unroll
-      for (int x = lane; x < D; x += 32) kq = fmaf(w[x], w[D + x], kq);
+      for (int x = lane; x < D; x += 32) kq = fmaf(to_f32(w.k[x]), to_f32(w.q[x]), kq);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) kq += __shfl_xor_sync(0xffffffffu, kq, d);
-      float4 O = *reinterpret_cast<const float4*>(rd + R::NW * D + c4);
-#pragma unroll
-      for (int x = 1; x < R::NW; ++x) {
-        const float4 y = *reinterpret_cast<const float4*>(rd + (R::NW + x) * D + c4);
-        O.x += y.x; O.y += y.y; O.z += y.z; O.w += y.w;
-      }
+      float4 O = collect(rd + R::NW * D);
       O.x = fmaf(kq, u.x, O.x); O.y = fmaf(kq, u.y, O.y); O.z = fmaf(kq, u.z, O.z); O.w = fmaf(kq, u.w, O.w);
       if (O.x != O.x || O.y != O.y || O.z != O.z || O.w != O.w) st |= ST_NAN;
-      if (rsub == 0) {
-        T* op = out + t * out_step + c4;
-        store4(op, O);
-      }
+      if (rsub == 0) store4(out + t * out_step + c4, O);
     }
 #pragma unroll
     for (int r4 = 0; r4 < R::RPT; r4 += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(w + row0 + r4);
+      const float4 k4 = load4(w.k + row0 + r4);
       const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        float4& t = S[r4 + y];
-        t.x = fmaf(kk[y], u.x, t.x); t.y = fmaf(kk[y], u.y, t.y);
-        t.z = fmaf(kk[y], u.z, t.z); t.w = fmaf(kk[y], u.w, t.w);
+        float4& x = S[r4 + y];
+        x.x = fmaf(kk[y], u.x, x.x); x.y = fmaf(kk[y], u.y, x.y);
+        x.z = fmaf(kk[y], u.z, x.z); x.w = fmaf(kk[y], u.w, x.w);
       }
     }
-    cur = nxt;
   }
 
-  if (PACKED) {
+  if (warp == 0) {
+    const RowTile t = answer(a, search, at, gridDim.x);
+    if (lane == 0) tiles[turn == 0 ? 2 : turn - 1] = t;
+  }
+  base += n;
+  fetch(nx, 0, base);
+  fetch(nx, 1, base + 1);
+  if (c.what & TILE_RUN) {
+    if (PACKED) {
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r) * D + c4) = S[r];
-    st |= pack_state<D>(a, h, record, rec, Ssh, [] { __syncthreads(); });  // its first barrier orders S
-  } else {
+      for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r) * D + c4) = S[r];
+      uint8_t* rec_out = rec_in + (a.rec_cap + 127) / 128 * 128;
+      st |= pack_state<D>(a, c.h, record_of(c), rec_out, Ssh, [] { __syncthreads(); });  // its first barrier orders S
+    } else {
+      float* S_pool = state_of(c);
 #pragma unroll
-    for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(S_pool + (size_t)(row0 + r) * D + c4) = S[r];
+      for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(S_pool + (size_t)(row0 + r) * D + c4) = S[r];
+    }
+  }
+  __syncthreads();  // the rows' vectors and the staged state have been read
   }
   if (st) atomicOr(a.t.status, st);
 }
