@@ -40,12 +40,10 @@ constexpr int kCoefFloats = 4 * 64 + 4;                      // e^G, beta, beta 
 constexpr int kPrepBytes = kTermsBytes + 4 * kCoefFloats;    // per block and value head
 static_assert(kPrepBytes % 16 == 0, "bulk copies move 16-byte multiples");
 
-// Terms 0 and 1 hold T and P T together: for each 16 columns kk = j / 16, the
-// operand rows that are not all zero there, rows 16 kk .. 63 of T in order,
-// then rows 63 .. 16 kk of P T backwards, so that the 128 - 32 kk result
-// columns are contiguous (u_16kk .. u_63, then o_63 .. o_16kk). Term 2 is T
-// alone. Rows come in groups of 8 x 16 columns, a group as two 8 x 8 pieces
-// of 128 contiguous bytes (the tensor core's unswizzled layout).
+// Terms 0 and 1 hold T and P T: for each 16 columns kk = j / 16, the operand
+// rows that are not all zero there, rows 16 kk .. 63 of T, then the same rows
+// of P T. Term 2 is T alone. Rows come in groups of 8 x 16 columns, a group as
+// two 8 x 8 pieces of 128 contiguous bytes (the tensor core's unswizzled layout).
 __host__ __device__ constexpr int term_base(int s) { return s * 2 * kTriBytes; }
 __host__ __device__ constexpr int pair_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }  // within terms 0, 1
 __host__ __device__ constexpr int tri_base(int kk) { return pair_base(kk) / 2; }                 // within term 2
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
       for (int z = 0; z < 4; ++z) {
         uint32_t t[kOutTerms];
         split2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1], t);
-        uint8_t* o2 = rec + row_piece(127 - 16 * (pi + pj) - r4 - 8 * (z & 1), 8 * (z >> 1) + j2) + pair_base(pj);
+        uint8_t* o2 = rec + row_piece(64 + 16 * (pi - 2 * pj) + r4 + 8 * (z & 1), 8 * (z >> 1) + j2) + pair_base(pj);
         *reinterpret_cast<uint32_t*>(o2 + term_base(0)) = t[0];
         *reinterpret_cast<uint32_t*>(o2 + term_base(1)) = t[1];
       }

@@ -40,7 +40,8 @@ constexpr int kMoveWarp = kScanCompute / 32, kProductWarp = kMoveWarp + 1;
 constexpr int kScanStages = 2;
 constexpr uint32_t kTileBytes = 64 * 128 * 2;  // q, k, v or o rows of a block
 // A stage: channels 0..63 of the q rows, then of the k rows, the same for
-// channels 64..127 (128-byte swizzled), the v rows, the prepared block.
+// channels 64..127, channels 0..63 and 64..127 of the v rows (all 128-byte
+// swizzled: 16-byte piece x of row r is at x ^ (r & 7)), the prepared block.
 constexpr uint32_t kStageV = 2 * kTileBytes, kStagePrep = 3 * kTileBytes;
 constexpr uint32_t kStageBytes = kStagePrep + (kPrepBytes + 1023) / 1024 * 1024;
 constexpr uint32_t kStageTx = kStagePrep + kPrepBytes;
@@ -55,6 +56,11 @@ struct ScanCtl {
 };
 constexpr size_t kScanSmem = 1024 + kOutAt + kTileBytes + sizeof(ScanCtl) + 16;
 
+// Byte offset of 16-byte piece x of row r in a tile of v or o rows.
+__device__ __forceinline__ int tile_piece(int r, int x) {
+  return (x >> 3) * (kTileBytes / 2) + r * 128 + (((x & 7) ^ (r & 7)) << 4);
+}
+
 struct ScanArgs {
   PrepArgs p;
 };
@@ -64,7 +70,7 @@ constexpr uint32_t TM_S = 0;      // S^T terms hi and mid, over D3: 16 columns f
 constexpr uint32_t TM_RU = 192;   // r^T terms, then u^T terms
 constexpr uint32_t TM_D1Q = 288;  // S^T q^T
 constexpr uint32_t TM_D1K = 352;  // S^T k^T
-constexpr uint32_t TM_D2 = 352;   // u^T (over S^T k^T), then the P T part of o, rows backwards
+constexpr uint32_t TM_D2 = 352;   // u^T (over S^T k^T), then the P T part of o
 
 // Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
 __host__ __device__ constexpr uint32_t s_col(int s, int ks) {
@@ -124,6 +130,29 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&x)[8]) {
                : "memory");
 }
 
+// The same by fragments, as the warp-wide matrix instructions lay out a
+// result: 16 lanes from `addr`'s on, 16 columns; this lane gets rows lane / 4
+// (x[4 g], x[4 g + 1]) and + 8 (x[4 g + 2], x[4 g + 3]), columns 8 g + 2
+// (lane % 4), + 1.
+__device__ __forceinline__ void tc_ld_frag(uint32_t (&x)[8], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : SQ_R8(x, 0) : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&x)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SQ_RW8(x, 0)::"memory");
+}
+// 8 columns of 32 bits: rows lane / 4 (x[2 g]) and + 8 (x[2 g + 1]), column 4 g + lane % 4.
+__device__ __forceinline__ void tc_st_frag(uint32_t addr, const uint32_t (&x)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3])
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix4t(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(sqk::smem_u32(p)), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // fp32 accumulators, bf16 operands, M = 128, N columns; `mn`: B has N contiguous.
 __host__ __device__ constexpr uint32_t mma_desc(uint32_t N, bool mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((128u >> 4) << 24);
@@ -147,6 +176,24 @@ __device__ __forceinline__ void put_terms(const float (&x)[16], uint32_t hi, uin
   tc_st8(hi, t[0]);
   tc_st8(mid, t[1]);
   tc_st8(lo, t[2]);
+}
+
+// A warp's 32 value columns x 16 rows of r or u, as fragments (x[h][...] the
+// 16 lanes 16 h on), to tensor memory as three terms, 32 columns apart.
+__device__ __forceinline__ void put_frag(const float (&x)[2][8], uint32_t to) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t t[kTerms][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[kTerms];
+      split3(x[h][2 * i], x[h][2 * i + 1], w);
+#pragma unroll
+      for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
+    }
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s) tc_st_frag(to + ((uint32_t)(16 * h) << 16) + 32 * s, t[s]);
+  }
 }
 
 // A warp's arrival on a barrier once its tensor memory stores are done.
@@ -240,55 +287,56 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const uint64_t ns = a.wait_ns;
   uint32_t st = 0;
 
-  if (warp == kMoveWarp) {  // ------------------------------------- loads and stores
-    if (lane == 0) {
-      int issued = 0;
-      auto load = [&](int i) {
-        const int sg = i & 1;
-        uint8_t* stage = smem + sg * kStageBytes;
+  if (warp == kMoveWarp) {  // ------------------------------- loads and stores
+    int issued = 0;
+    auto load = [&](int i) {
+      const int sg = i & 1;
+      uint8_t* stage = smem + sg * kStageBytes;
+      const int row = first + 64 * i;
+      if (lane == 0) {
         sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx);
-        const int row = first + 64 * i;
         tma_tile(stage + kTileBytes / 2, &k_map, 0, hk, row, &ctl.full[sg]);
         tma_tile(stage + 3 * kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
         tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
         tma_tile(stage + kTileBytes, &q_map, 64, hk, row, &ctl.full[sg]);
         tma_tile(stage + kStageV, &v_map, 0, h, row, &ctl.full[sg]);
+        tma_tile(stage + kStageV + kTileBytes / 2, &v_map, 64, h, row, &ctl.full[sg]);
         sqk::bulk_g2s(stage + kStagePrep, args.p.ws + ((uint64_t)(c0 + i) * a.h_v + h) * kPrepBytes, kPrepBytes,
                       &ctl.full[sg]);
-        issued = i + 1;
-      };
-      load(0);
-      if (blocks > 1) load(1);
-      for (int i = 0; i < blocks; ++i) {
-        // block i's stage is free when its D3 is done; its o follows
-        if (i + kScanStages < blocks) {
-          if (!sqk::mbar_wait_bounded(&ctl.empty[i & 1], (i >> 1) & 1, ns)) {
-            ctl.abort = 1;
-            break;
-          }
-          load(i + kScanStages);
-        }
-        if (!sqk::mbar_wait_bounded(&ctl.o_ready, i & 1, ns)) {
-          ctl.abort = 1;
-          break;
-        }
-        const int live = n - 64 * i;
-        if (live >= 64) {
+      }
+      issued = i + 1;
+    };
+    load(0);
+    if (blocks > 1) load(1);
+    for (int i = 0; i < blocks; ++i) {
+      // block i's stage is free when its D3 is done; its o follows
+      if (i + kScanStages < blocks) {
+        if (!warp_wait(ctl, &ctl.empty[i & 1], (i >> 1) & 1, ns)) break;
+        load(i + kScanStages);
+      }
+      if (!warp_wait(ctl, &ctl.o_ready, i & 1, ns)) break;
+      const int live = n - 64 * i;
+      if (live >= 64) {
+        if (lane == 0) {
           tma_store(&o_map, 0, h, first + 64 * i, smem + kOutAt);
+          tma_store(&o_map, 64, h, first + 64 * i, smem + kOutAt + kTileBytes / 2);
           sqk::bulk_commit();
           sqk::bulk_wait_read_all();
-        } else {  // the last block: its live rows only
-          for (int y = 0; y < live; ++y)
-            sqk::bulk_s2g(out + ((size_t)(first + 64 * i + y) * a.h_v + h) * 128, smem + kOutAt + 256 * y, 256);
-          sqk::bulk_commit();
         }
-        sqk::mbar_arrive(&ctl.o_free);
+      } else {  // the last block: its live rows only
+        for (int y = lane; y < live * 16; y += 32) {
+          const int row = y >> 4, piece = y & 15;
+          reinterpret_cast<uint4*>(out + ((size_t)(first + 64 * i + row) * a.h_v + h) * 128)[piece] =
+              *reinterpret_cast<const uint4*>(smem + kOutAt + tile_piece(row, piece));
+        }
       }
-      // no copy is in flight when the CTA ends
-      for (int i = max(0, issued - kScanStages); i < issued; ++i)
-        sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
-      sqk::bulk_wait_all();
+      __syncwarp();
+      if (lane == 0) sqk::mbar_arrive(&ctl.o_free);
     }
+    // no copy is in flight when the CTA ends
+    for (int i = max(0, issued - kScanStages); i < issued; ++i)
+      sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
+    if (lane == 0) sqk::bulk_wait_all();
   } else if (warp == kProductWarp) {  // ------------------------------------- products
     const uint32_t base = sqk::smem_u32(smem);
     for (int i = 0; i < blocks; ++i) {
@@ -341,7 +389,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         for (int x = 3; x < 6; ++x)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // P T follows T's 64 - 16 kk rows, 32 bytes each
-            tc_mma(tm + TM_D2 + 64, tm + TM_RU + 32 * pr[x] + 8 * kk,
+            tc_mma(tm + TM_D2 + 64 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk,
                    prep + (term_base(pt[x]) + pair_base(kk) + 32 * (64 - 16 * kk)) / 16, mma_desc(64 - 16 * kk, false),
                    x > 3 || kk > 0);
         tc_commit(&ctl.d2o);
@@ -375,10 +423,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       put_terms(S[y], hi, hi + 8, tl + TM_S + 128 + 32 * y + 8 * part);
       warp_arrive(&ctl.s_ready[y]);
     };
-    const uint32_t ru = tl + TM_RU + 8 * part;  // r and u of rows 16 part .. + 15
+    // r, u and o go by fragments: rows j = 16 part + 8 g + 2 (lane % 4), + 1 of value columns lane / 4 + 8 m of the warp's
+    const uint32_t ru = tl + TM_RU + 8 * part;
+    constexpr uint32_t upper = 16u << 16;                         // the warp's lanes 16..31
+    const int j2 = 16 * part + 2 * (lane & 3);                    // first of this lane's rows
+    const int at = tile_piece(16 * part + (lane & 7), 4 * (warp & 3) + (lane >> 3));  // of v or o: a matrix's row; g: + 1024
     put_state(0);
     put_state(1);
-    float x[16];
+    float x[2][8];
     // block i's rows: beta v into x; false where the wait ran out
     auto take_rows = [&](int i) {
       if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns)) return false;
@@ -391,91 +443,104 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                                     (y & 7) * 16) = make_uint4(0, 0, 0, 0);
         sqk::fence_proxy_async_smem();
       }
-      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + kStageV) + 16 * part * 128 + col;
-      const float4* eb = reinterpret_cast<const float4*>(stage + kStagePrep + kTermsBytes) + 16 + 4 * part;
+      const float* beta = reinterpret_cast<const float*>(stage + kStagePrep + kTermsBytes) + 64 + j2;
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 e = eb[j >> 2];
-        x[j] = e.x * __bfloat162float(v[j * 128]);
-        x[j + 1] = e.y * __bfloat162float(v[(j + 1) * 128]);
-        x[j + 2] = e.z * __bfloat162float(v[(j + 2) * 128]);
-        x[j + 3] = e.w * __bfloat162float(v[(j + 3) * 128]);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t v[4];
+        ldmatrix4t(v, stage + kStageV + at + 1024 * g);
+        const float2 e = *reinterpret_cast<const float2*>(beta + 8 * g);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          x[m >> 1][4 * g + 2 * (m & 1)] = e.x * __uint_as_float(v[m] << 16);
+          x[m >> 1][4 * g + 2 * (m & 1) + 1] = e.y * __uint_as_float(v[m] & 0xffff0000u);
+        }
       }
       return true;
     };
     bool ok = take_rows(0);
     for (int i = 0; i < blocks && ok; ++i) {
       const uint32_t ph = i & 1;
-      const int live = min(64, n - 64 * i), mine = live - 16 * part;  // rows; of this thread
+      const int live = min(64, n - 64 * i);
       const float* coef = reinterpret_cast<const float*>(smem + (i & 1) * kStageBytes + kStagePrep + kTermsBytes);
-      const float4* eg = reinterpret_cast<const float4*>(coef + 16 * part);  // e^G; 16 float4s on: beta, beta e^G, e^(G63 - G)
-      uint32_t w[16];
+      uint32_t w[2][8];
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
-      tc_ld16(w, tl + TM_D1K + 16 * part);
-      tc_wait_ld(w);
+      tc_ld_frag(w[0], tl + TM_D1K + 16 * part);
+      tc_ld_frag(w[1], tl + upper + TM_D1K + 16 * part);
+      tc_wait_ld(w[0]);
+      tc_wait_ld(w[1]);
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 e = eg[32 + (j >> 2)];
-        x[j] = fmaf(-e.x, __uint_as_float(w[j]), x[j]);
-        x[j + 1] = fmaf(-e.y, __uint_as_float(w[j + 1]), x[j + 1]);
-        x[j + 2] = fmaf(-e.z, __uint_as_float(w[j + 2]), x[j + 2]);
-        x[j + 3] = fmaf(-e.w, __uint_as_float(w[j + 3]), x[j + 3]);
-      }
-      if (live < 64) {  // whatever the rows behind the last held
+      for (int g = 0; g < 2; ++g) {
+        const float2 e = *reinterpret_cast<const float2*>(coef + 128 + j2 + 8 * g);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = j < mine ? x[j] : 0.0f;
+        for (int m = 0; m < 4; ++m) {
+          float* y = &x[m >> 1][4 * g + 2 * (m & 1)];
+          y[0] = fmaf(-e.x, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]), y[0]);
+          y[1] = fmaf(-e.y, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]), y[1]);
+          if (live < 64) {  // whatever the rows behind the last held
+            if (j2 + 8 * g >= live) y[0] = 0.0f;
+            if (j2 + 8 * g + 1 >= live) y[1] = 0.0f;
+          }
+        }
       }
-      put_terms(x, ru, ru + 32, ru + 64);
+      put_frag(x, ru);
       warp_arrive(&ctl.r_ready);
 
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
       tc_after();
-      tc_ld16(w, tl + TM_D2 + 16 * part);
-      tc_wait_ld(w);
+      tc_ld_frag(w[0], tl + TM_D2 + 16 * part);
+      tc_ld_frag(w[1], tl + upper + TM_D2 + 16 * part);
+      tc_wait_ld(w[0]);
+      tc_wait_ld(w[1]);
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 e = eg[48 + (j >> 2)];
-        x[j] = e.x * __uint_as_float(w[j]);
-        x[j + 1] = e.y * __uint_as_float(w[j + 1]);
-        x[j + 2] = e.z * __uint_as_float(w[j + 2]);
-        x[j + 3] = e.w * __uint_as_float(w[j + 3]);
+      for (int g = 0; g < 2; ++g) {
+        const float2 e = *reinterpret_cast<const float2*>(coef + 192 + j2 + 8 * g);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          x[m >> 1][4 * g + 2 * (m & 1)] = e.x * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]);
+          x[m >> 1][4 * g + 2 * (m & 1) + 1] = e.y * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]);
+        }
       }
       // u's terms take r's place when the P T products have read it
       if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
-      put_terms(x, ru, ru + 32, ru + 64);
+      put_frag(x, ru);
       warp_arrive(&ctl.u_ready);
 
       // under the state's product: o on its way out, the next block's rows in
       if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
       {
-        uint32_t y[16];
+        uint32_t y[2][8];
         tc_after();
-        tc_ld16(w, tl + TM_D1Q + 16 * part);
-        tc_ld16(y, tl + TM_D2 + 112 - 16 * part);
-        tc_wait_ld(w);
-        tc_wait_ld(y);
-        uint16_t* op = reinterpret_cast<uint16_t*>(smem + kOutAt) + 16 * part * 128 + col;
-        float bad = 0.0f;  // stays 0 while every o is finite
+        tc_ld_frag(w[0], tl + TM_D1Q + 16 * part);
+        tc_ld_frag(w[1], tl + upper + TM_D1Q + 16 * part);
+        tc_ld_frag(y[0], tl + TM_D2 + 64 + 16 * part);
+        tc_ld_frag(y[1], tl + upper + TM_D2 + 64 + 16 * part);
+        tc_wait_ld(w[0]);
+        tc_wait_ld(w[1]);
+        tc_wait_ld(y[0]);
+        tc_wait_ld(y[1]);
+        uint32_t o[2][4];
+        __nv_bfloat162 bad = __float2bfloat162_rn(0.0f);  // stays 0 while every o is finite
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 e = eg[j >> 2];
-          x[j] = fmaf(e.x, __uint_as_float(w[j]), __uint_as_float(y[15 - j]));
-          x[j + 1] = fmaf(e.y, __uint_as_float(w[j + 1]), __uint_as_float(y[14 - j]));
-          x[j + 2] = fmaf(e.z, __uint_as_float(w[j + 2]), __uint_as_float(y[13 - j]));
-          x[j + 3] = fmaf(e.w, __uint_as_float(w[j + 3]), __uint_as_float(y[12 - j]));
+        for (int g = 0; g < 2; ++g) {
+          const float2 e = *reinterpret_cast<const float2*>(coef + j2 + 8 * g);
 #pragma unroll
-          for (int z = j; z < j + 4; z += 2) {
-            bad = fmaf(x[z], 0.0f, fmaf(x[z + 1], 0.0f, bad));
-            const uint32_t t = bf16x2(x[z], x[z + 1]);
-            op[z * 128] = (uint16_t)t;
-            op[(z + 1) * 128] = (uint16_t)(t >> 16);
+          for (int m = 0; m < 4; ++m) {
+            const int z = 4 * g + 2 * (m & 1);
+            o[g][m] = bf16x2(fmaf(e.x, __uint_as_float(w[m >> 1][z]), __uint_as_float(y[m >> 1][z])),
+                             fmaf(e.y, __uint_as_float(w[m >> 1][z + 1]), __uint_as_float(y[m >> 1][z + 1])));
+            bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&o[g][m]), __float2bfloat162_rn(0.0f), bad);
           }
+          stmatrix4t(smem + kOutAt + at + 1024 * g, o[g][0], o[g][1], o[g][2], o[g][3]);
         }
-        if (bad != 0.0f) {  // an infinity or a NaN: a NaN in a live row is reported
+        if (*reinterpret_cast<const uint32_t*>(&bad) != 0) {  // an infinity or a NaN: a NaN in a live row is reported
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < mine && x[j] != x[j]) st |= ST_NAN;
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (((o[g][m] & 0x7fffu) > 0x7f80u && j2 + 8 * g < live) ||
+                  ((o[g][m] & 0x7fffffffu) > 0x7f80ffffu && j2 + 8 * g + 1 < live))
+                st |= ST_NAN;
         }
       }
       sqk::fence_proxy_async_smem();
@@ -489,10 +554,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         if (!ok) break;
         tc_after();
         if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[i & 1]);  // this warp's reads of the stage came before
-        tc_ld16(w, tl + TM_S + 64 * y + 16 * part);
-        tc_wait_ld(w);
+        uint32_t d[16];
+        tc_ld16(d, tl + TM_S + 64 * y + 16 * part);
+        tc_wait_ld(d);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[y][j] = fmaf(g63, S[y][j], __uint_as_float(w[j]));
+        for (int j = 0; j < 16; ++j) S[y][j] = fmaf(g63, S[y][j], __uint_as_float(d[j]));
         if (i + 1 < blocks) put_state(y);
       }
     }

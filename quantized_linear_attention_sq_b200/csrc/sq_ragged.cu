@@ -121,8 +121,8 @@ bool in_blocks(const sq_handle* h, int dtype, int32_t max_len) {
   return dtype == SQ_BF16 && h->desc.gate == SQ_GATE_HEAD && h->d == 128 && max_len >= kMinLong;
 }
 
-// Tensor map of a [rows, heads, 128] bf16 matrix: boxes of 64 rows of one
-// head, `cols` columns wide, rows behind the last read as zeros.
+// Tensor map of a [rows, heads, 128] bf16 matrix: boxes of 64 rows and 64
+// channels of one head, rows behind the last read as zeros.
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -137,16 +137,15 @@ EncodeTiled encode_tiled() {
   }();
   return fn;
 }
-sq_status row_map(CUtensorMap* m, const char* name, const void* p, int64_t stride, int heads, int32_t rows, int cols,
-                  CUtensorMapSwizzle swizzle) {
+sq_status row_map(CUtensorMap* m, const char* name, const void* p, int64_t stride, int heads, int32_t rows) {
   const EncodeTiled enc = encode_tiled();
   if (!enc) return fail(SQ_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
   if (rows == 1) stride = (int64_t)heads * 128;  // never used, but must be valid
   const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)cols, 1, 64}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, 64}, one[3] = {1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SQ_OK : fail(SQ_ERR_CUDA, "tensor map of %s: driver error %d", name, (int)r);
 }
@@ -160,10 +159,10 @@ sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_r
   a.p.ws = static_cast<uint8_t*>(workspace);
   a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
   CUtensorMap qm, km, vm, om;
-  sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-  if (s == SQ_OK) s = row_map(&om, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+  sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows);
+  if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows);
+  if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows);
+  if (s == SQ_OK) s = row_map(&om, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows);
   if (s != SQ_OK) return s;
   static std::atomic<uint64_t> seen_prepare{0}, seen_fp32{0}, seen_packed{0};
   auto scan = r.fmt_fp32 ? sqr::k_chunk_scan<false> : sqr::k_chunk_scan<true>;
