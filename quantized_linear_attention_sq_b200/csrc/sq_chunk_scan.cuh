@@ -65,12 +65,14 @@ struct ScanArgs {
   PrepArgs p;
 };
 
-// Columns of tensor memory (480 of 512).
+// Columns of tensor memory (all 512).
 constexpr uint32_t TM_S = 0;      // S^T terms hi and mid, over D3: 16 columns for each 16 key rows; lo from 128 on
-constexpr uint32_t TM_RU = 192;   // r^T terms, then u^T terms
+constexpr uint32_t TM_R = 192;    // r^T terms
 constexpr uint32_t TM_D1Q = 288;  // S^T q^T
 constexpr uint32_t TM_D1K = 352;  // S^T k^T
 constexpr uint32_t TM_D2 = 352;   // u^T (over S^T k^T), then the P T part of o
+// u^T terms: two over the lo terms of S^T, which D1 has read, one behind the rest.
+__host__ __device__ constexpr uint32_t u_col(int s) { return s == 2 ? 480u : 128u + 32u * s; }
 
 // Column of term s of S^T for key rows 16 ks .. 16 ks + 15.
 __host__ __device__ constexpr uint32_t s_col(int s, int ks) {
@@ -182,24 +184,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
          (1ull << 46) | (swizzle << 61);
 }
 
-// 16 fp32 values of a lane (k index 0..15 of an A operand) to tensor memory as three terms.
-__device__ __forceinline__ void put_terms(const float (&x)[16], uint32_t hi, uint32_t mid, uint32_t lo) {
-  uint32_t t[kTerms][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w[kTerms];
-    split_a(x[2 * i], x[2 * i + 1], w);
-#pragma unroll
-    for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
-  }
-  tc_st8(hi, t[0]);
-  tc_st8(mid, t[1]);
-  tc_st8(lo, t[2]);
-}
-
 // A warp's 32 value columns x 16 rows of r or u, as fragments (x[h][...] the
-// 16 lanes 16 h on), to tensor memory as three terms, 32 columns apart.
-__device__ __forceinline__ void put_frag(const float (&x)[2][8], uint32_t to) {
+// 16 lanes 16 h on), to tensor memory as three terms.
+__device__ __forceinline__ void put_frag(const float (&x)[2][8], uint32_t hi, uint32_t mid, uint32_t lo) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t t[kTerms][4];
@@ -210,8 +197,10 @@ __device__ __forceinline__ void put_frag(const float (&x)[2][8], uint32_t to) {
 #pragma unroll
       for (int s = 0; s < kTerms; ++s) t[s][i] = w[s];
     }
-#pragma unroll
-    for (int s = 0; s < kTerms; ++s) tc_st_frag(to + ((uint32_t)(16 * h) << 16) + 32 * s, t[s]);
+    const uint32_t lanes = (uint32_t)(16 * h) << 16;
+    tc_st_frag(hi + lanes, t[0]);
+    tc_st_frag(mid + lanes, t[1]);
+    tc_st_frag(lo + lanes, t[2]);
   }
 }
 
@@ -400,7 +389,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         for (int x = 0; x < 6; ++x)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk,
+            tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
                    prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16,
                    mma_desc(64 - 16 * kk, false, pr[x]), x > 0 || kk > 0);
         tc_commit(&ctl.d2);
@@ -408,7 +397,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         for (int x = 3; x < 6; ++x)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // P T follows T's 64 - 16 kk rows, 32 bytes each
-            tc_mma(tm + TM_D2 + 64 + 16 * kk, tm + TM_RU + 32 * pr[x] + 8 * kk,
+            tc_mma(tm + TM_D2 + 64 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
                    prep + (term_base(pt[x]) + pair_base(kk) + 32 * (64 - 16 * kk)) / 16,
                    mma_desc(64 - 16 * kk, false, pr[x]), x > 3 || kk > 0);
         tc_commit(&ctl.d2o);
@@ -424,7 +413,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           for (int s = kTerms - 1; s >= 0; --s)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma(tm + TM_S + 64 * x, tm + TM_RU + 32 * s + 8 * kk, km + (x * kTileBytes + kk * 2048) / 16,
+              tc_mma(tm + TM_S + 64 * x, tm + u_col(s) + 8 * kk, km + (x * kTileBytes + kk * 2048) / 16,
                      mma_desc(64, true, s), s < kTerms - 1 || kk > 0);
           tc_commit(&ctl.d3[x]);
         }
@@ -437,18 +426,32 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     warp_wait(ctl, &ctl.drain, 0, ns);
   } else {  // -------------------------------------------------- the rest
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    auto put_state = [&](int y) {
-      const uint32_t hi = tl + TM_S + 64 * y + 16 * part;
-      put_terms(S[y], hi, hi + 8, tl + TM_S + 128 + 32 * y + 8 * part);
+    auto split_state = [&](int y, uint32_t (&t)[kTerms][8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t z[kTerms];
+        split_a(S[y][2 * j], S[y][2 * j + 1], z);
+#pragma unroll
+        for (int s = 0; s < kTerms; ++s) t[s][j] = z[s];
+      }
+    };
+    auto put_state = [&](int y, const uint32_t (&t)[kTerms][8]) {
+      const uint32_t to = tl + TM_S + 16 * part;
+      tc_st8(to + 64 * y, t[0]);
+      tc_st8(to + 64 * y + 8, t[1]);
+      tc_st8(tl + TM_S + 128 + 32 * y + 8 * part, t[2]);
       warp_arrive(&ctl.s_ready[y]);
     };
     // r, u and o go by fragments: rows j = 16 part + 8 g + 2 (lane % 4), + 1 of value columns lane / 4 + 8 m of the warp's
-    const uint32_t ru = tl + TM_RU + 8 * part;
+    const uint32_t rt = tl + TM_R + 8 * part, ut = tl + 8 * part;
     constexpr uint32_t upper = 16u << 16;                         // the warp's lanes 16..31
     const int j2 = 16 * part + 2 * (lane & 3);                    // first of this lane's rows
     const int at = tile_piece(16 * part + (lane & 7), 4 * (warp & 3) + (lane >> 3));  // of v or o: a matrix's row; g: + 1024
-    put_state(0);
-    put_state(1);
+    for (int y = 0; y < 2; ++y) {
+      uint32_t t[kTerms][8];
+      split_state(y, t);
+      put_state(y, t);
+    }
     float x[2][8];
     // block i's rows: beta v into x; false where the wait ran out
     auto take_rows = [&](int i) {
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           }
         }
       }
-      put_frag(x, ru);
+      put_frag(x, rt, rt + 32, rt + 64);
       warp_arrive(&ctl.r_ready);
 
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
@@ -520,12 +523,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           x[m >> 1][4 * g + 2 * (m & 1) + 1] = e.y * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]);
         }
       }
-      // u's terms take r's place when the P T products have read it
-      if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
-      put_frag(x, ru);
+      put_frag(x, ut + u_col(0), ut + u_col(1), ut + u_col(2));
       warp_arrive(&ctl.u_ready);
 
-      // under the state's product: o on its way out, the next block's rows in
+      // o, under the state's product
+      if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
       if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
       {
         uint32_t y[2][8];
@@ -566,20 +568,28 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       __syncwarp();
       if (lane == 0) sqk::mbar_arrive(&ctl.o_ready);
       const float g63 = coef[256];
-      if (i + 1 < blocks) ok = take_rows(i + 1);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         ok = ok && warp_wait(ctl, &ctl.d3[y], ph, ns);
         if (!ok) break;
         tc_after();
-        if (y == 1 && lane == 0) sqk::mbar_arrive(&ctl.empty[i & 1]);  // this warp's reads of the stage came before
         uint32_t d[16];
         tc_ld16(d, tl + TM_S + 64 * y + 16 * part);
         tc_wait_ld(d);
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[y][j] = fmaf(g63, S[y][j], __uint_as_float(d[j]));
-        if (i + 1 < blocks) put_state(y);
+        if (i + 1 < blocks) {
+          uint32_t t[kTerms][8];
+          split_state(y, t);
+          // the lo terms go where the second half of D3 still reads u
+          if (y == 0) ok = warp_wait(ctl, &ctl.d3[1], ph, ns);
+          if (!ok) break;
+          put_state(y, t);
+        }
       }
+      // under the next block's first product: its rows
+      if (lane == 0) sqk::mbar_arrive(&ctl.empty[i & 1]);  // this warp's reads of the stage came before
+      if (ok && i + 1 < blocks) ok = take_rows(i + 1);
     }
   }
   tc_before();
