@@ -14,8 +14,8 @@
 // gates are summed as pairs of fp32: a difference G_i - G_j keeps its
 // precision behind a gate of zero. Decays are products of factors that are
 // all at most one (token to the end of its 16, from the start of its 16,
-// between 16s; formed pair by pair inside a 16), so a block needs a fourth of
-// the exponentials. The inverse goes by blocks of 16: those on the diagonal
+// between 16s; inside a 16 the quotient of two of them), so a block needs a
+// few hundred exponentials, not one for each pair. The inverse goes by blocks of 16: those on the diagonal
 // by substitution in fp32, then pairs of blocks, [T1 0; -T2 A21 T1, T2], to
 // 32 and to 64 on the tensor cores, every operand as three bf16 terms whose
 // sum is the fp32 value (the six largest of nine products: fp32 accuracy).
@@ -73,29 +73,31 @@ __device__ __forceinline__ bool block_span(const PrepArgs& a, int c, int& first,
   return true;
 }
 
-// x = hi + mid + lo exactly, each a bf16: an fp32 value's 24 significant bits
-// are three times 8, cut off one after the other. Two values at a time,
-// packed as (a: low half, b: high half).
-__device__ __forceinline__ uint32_t pack_high(float a, float b) {
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[kTerms]) {
-  t[0] = pack_high(a, b);
-  a = __fsub_rn(a, cut(a));
-  b = __fsub_rn(b, cut(b));
-  t[1] = pack_high(a, b);
-  t[2] = pack_high(__fsub_rn(a, cut(a)), __fsub_rn(b, cut(b)));
-}
-__device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // rounded to nearest
+// x = hi + mid + lo, each a bf16 rounded to nearest: an fp32 value's 24
+// significant bits are three times 8. Two values at a time, packed as (a: low
+// half, b: high half). The remainders are fused multiply-adds with a bf16
+// operand as it is: 7 instructions, where cutting and packing takes 11.
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-// The first two terms only, the second rounded to nearest.
+__device__ __forceinline__ uint32_t take_bf16x2(float& a, float& b) {  // leaves the remainders
+  const uint32_t t = bf16x2(a, b);
+  asm("{\n\t.reg .b16 l, h, m;\n\tmov.b16 m, 0xBF80;\n\tmov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, h, m, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(t));
+  return t;
+}
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[kTerms]) {
+  t[0] = take_bf16x2(a, b);
+  t[1] = take_bf16x2(a, b);
+  t[2] = bf16x2(a, b);
+}
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[kOutTerms]) {
-  t[0] = pack_high(a, b);
-  t[1] = bf16x2(__fsub_rn(a, cut(a)), __fsub_rn(b, cut(b)));
+  t[0] = take_bf16x2(a, b);
+  t[1] = bf16x2(a, b);
 }
 
 constexpr int kPrepThreads = 128;
@@ -112,7 +114,9 @@ struct PrepGate {
   float beta[64];
   float from[64];    // e^(G_i - R_(b-1))  from its 16's start
   float to[64];      // e^(R_b - G_j)      to its 16's end
+  float inv[64];     // 1 / from
   float hop[4][4];   // e^(R_(bi-1) - R_bj), bj < bi
+  int32_t steep[4];  // the 16's decay is below 2^-100: its inverses may overflow, its pairs are formed one by one
 };
 struct PrepSmem {
   union {
@@ -179,16 +183,16 @@ __device__ __forceinline__ void acc_terms(const Acc& acc, Terms& t) {
     for (int s = 0; s < kTerms; ++s) t[s][x] = w[s];
   }
 }
-__device__ __forceinline__ void put_left(uint8_t* block, const uint32_t (&t)[4]) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, at = 4 * (lane & 3);
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    *reinterpret_cast<uint32_t*>(block + blk_piece(r + 8 * (x & 1), x >> 1) + at) = t[x];
+// A left operand's registers to a block: `block` is at this lane's place in it
+// (row lane / 4, columns 2 (lane % 4)), `turn` (16 or -16) leads to columns + 8.
+__device__ __forceinline__ void put_left(uint8_t* block, int turn, const uint32_t (&t)[4]) {
+  *reinterpret_cast<uint32_t*>(block) = t[0];
+  *reinterpret_cast<uint32_t*>(block + 256) = t[1];
+  *reinterpret_cast<uint32_t*>(block + turn) = t[2];
+  *reinterpret_cast<uint32_t*>(block + turn + 256) = t[3];
 }
 
-// Row, column and number of the blocks on and below the diagonal.
-__device__ __forceinline__ int tri_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
-__device__ __forceinline__ int tri_col(int t) { return t - tri_row(t) * (tri_row(t) + 1) / 2; }
+// Number of a block on or below the diagonal, and of one below it.
 __device__ __forceinline__ int tri(int bi, int bj) { return bi * (bi + 1) / 2 + bj; }
 __device__ __forceinline__ int below(int bi, int bj) { return bi * (bi - 1) / 2 + bj; }
 
@@ -236,6 +240,8 @@ __device__ __forceinline__ void prepare_gates(const PrepArgs& a, PrepSmem& sm, u
   s.beta[i] = beta;
   s.from[i] = pow2(pair_diff(G, prev));
   s.to[i] = pow2(pair_diff(mine, G));
+  s.inv[i] = pow2(pair_diff(prev, G));
+  if ((i & 15) == 0) s.steep[i >> 4] = !(pair_diff(mine, prev) >= -100.0f);
   const int bi = (i >> 2) & 3, bj = i & 3;
   if (i < 16 && bj < bi) s.hop[bi][bj] = pow2(pair_diff(s.G[16 * bi - 1], s.G[16 * bj + 15]));
   if (on) {
@@ -268,12 +274,16 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
     *reinterpret_cast<uint4*>(&s.qk[which][row * kTile + 8 * piece]) = v;
   }
   __syncthreads();
-  // the ten blocks on and below the diagonal of q k^T (even items) and of
-  // k k^T (odd ones), five for each warp
+  // the ten blocks on and below the diagonal, of q k^T (even warps) and of
+  // k k^T (odd ones), five for each warp: every other one of the list
+  // 00 10 11 20 21 22 30 31 32 33
+  const int which = warp & 1, odd = warp >> 1;
+  constexpr int rows0[5] = {0, 1, 2, 3, 3}, cols0[5] = {0, 1, 1, 0, 2};
+  constexpr int rows1[5] = {1, 2, 2, 3, 3}, cols1[5] = {0, 0, 2, 1, 3};
   Acc dot[5];
 #pragma unroll
   for (int x = 0; x < 5; ++x) {
-    const int item = warp + 4 * x, which = item & 1, bi = tri_row(item >> 1), bj = tri_col(item >> 1);
+    const int bi = odd ? rows1[x] : rows0[x], bj = odd ? cols1[x] : cols0[x];
     dot[x].zero();
     const __nv_bfloat16* A = &s.qk[which][(16 * bi + (lane & 15)) * kTile + 8 * (lane >> 4)];
     const __nv_bfloat16* Bm = &s.qk[1][(16 * bj + (lane & 7) + 8 * (lane >> 4)) * kTile + 8 * ((lane >> 3) & 1)];
@@ -288,6 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
   const int share = a.r.h_v / a.r.h_k;
   const int j2 = 2 * (lane & 3), r4 = lane >> 2;
   const int piece = blk_piece(lane & 15, lane >> 4);  // this lane's row of a matrix load
+  const int left = blk_piece(r4, 0) + 2 * j2, turn = blk_piece(0, 1) - 2 * (blk_piece(r4, 0) & 16);  // see put_left
 #pragma unroll 1
   for (int hh = 0; hh < share; ++hh) {
     const int h = hk * share + hh;
@@ -297,42 +308,61 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
     __syncthreads();  // the factors; the tiles (first head) or the previous head's matrices have been read
 #pragma unroll
     for (int x = 0; x < 5; ++x) {
-      const int item = warp + 4 * x, which = item & 1, bi = tri_row(item >> 1), bj = tri_col(item >> 1);
+      const int bi = odd ? rows1[x] : rows0[x], bj = odd ? cols1[x] : cols0[x];
+      const bool diag = bi == bj;
+      const float* col = (diag ? gt.inv : gt.to) + 16 * bj + j2;
+      float2 c0 = *reinterpret_cast<const float2*>(col), c1 = *reinterpret_cast<const float2*>(col + 8);
+      const float hop = diag ? 1.0f : gt.hop[bi][bj];
       Acc m;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int i = 16 * bi + r4 + 8 * y;
-        float f = which ? gt.beta[i] : 1.0f;
-        float t[4];  // of columns j2, + 1, + 8, + 9
-        if (bi == bj) {
-          const float2 G = gt.G[i];
+        const float f = gt.from[i] * hop * (which ? gt.beta[i] : 1.0f);
+        m.c[0][2 * y] = f * c0.x * dot[x].c[0][2 * y];
+        m.c[0][2 * y + 1] = f * c0.y * dot[x].c[0][2 * y + 1];
+        m.c[1][2 * y] = f * c1.x * dot[x].c[1][2 * y];
+        m.c[1][2 * y + 1] = f * c1.y * dot[x].c[1][2 * y + 1];
+      }
+      if ((x == 0 || x == 1 || x == 2 || x == 4) && diag) {  // the others never are
+        if (gt.steep[bi]) {
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int lj = j2 + (z & 1) + 8 * (z >> 1);
-            t[z] = lj <= r4 + 8 * y ? pow2(pair_diff(G, gt.G[16 * bj + lj])) : 0.0f;
+          for (int z = 0; z < 8; ++z) {
+            const int li = r4 + 8 * ((z >> 1) & 1), lj = j2 + (z & 1) + 8 * (z >> 2);
+            const float e = lj <= li ? pow2(pair_diff(gt.G[16 * bi + li], gt.G[16 * bi + lj])) : 0.0f;
+            m.c[z >> 2][z & 3] = (which ? gt.beta[16 * bi + li] : 1.0f) * e * dot[x].c[z >> 2][z & 3];
           }
-        } else {
-          const float2 t0 = *reinterpret_cast<const float2*>(gt.to + 16 * bj + j2);
-          const float2 t1 = *reinterpret_cast<const float2*>(gt.to + 16 * bj + j2 + 8);
-          t[0] = t0.x, t[1] = t0.y, t[2] = t1.x, t[3] = t1.y;
-          f *= gt.from[i] * gt.hop[bi][bj];
         }
 #pragma unroll
-        for (int z = 0; z < 4; ++z) m.c[z >> 1][2 * y + (z & 1)] = f * t[z] * dot[x].c[z >> 1][2 * y + (z & 1)];
+        for (int z = 0; z < 8; ++z)  // above the diagonal: nothing, whatever the dots hold
+          if (j2 + (z & 1) + 8 * (z >> 2) > r4 + 8 * ((z >> 1) & 1)) m.c[z >> 2][z & 3] = 0.0f;
+        if (which) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<float2*>(&s.m.Ad[bi][r4 + 8 * y][j2 + 8 * z]) =
+                  make_float2(m.c[z][2 * y], m.c[z][2 * y + 1]);
+          continue;
+        }
       }
-      if (which && bi == bj) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-            *reinterpret_cast<float2*>(&s.m.Ad[bi][r4 + 8 * y][j2 + 8 * z]) = make_float2(m.c[z][2 * y], m.c[z][2 * y + 1]);
-      } else {
+      if (which) {
         Terms t;
         acc_terms(m, t);
-        uint8_t* dst = which ? s.m.A[below(bi, bj)][0] : s.m.P[tri(bi, bj)][0];
-        put_left(dst, t[0]);
-        put_left(dst + kBlk, t[1]);
-        if (which) put_left(dst + 2 * kBlk, t[2]);
+        uint8_t* dst = s.m.A[below(bi, bj)][0] + left;
+#pragma unroll
+        for (int u = 0; u < kTerms; ++u) put_left(dst + u * kBlk, turn, t[u]);
+      } else {
+        uint8_t* dst = s.m.P[tri(bi, bj)][0] + left;
+        uint32_t t0[4], t1[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          uint32_t w[kOutTerms];
+          split2(m.c[z >> 1][2 * (z & 1)], m.c[z >> 1][2 * (z & 1) + 1], w);
+          t0[z] = w[0];
+          t1[z] = w[1];
+        }
+        put_left(dst, turn, t0);
+        put_left(dst + kBlk, turn, t1);
       }
     }
     __syncthreads();
@@ -344,7 +374,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
       for (int i = 0; i < 16; ++i) {
         float acc = i == col ? 1.0f : 0.0f;
 #pragma unroll
-        for (int l = 0; l < i; ++l) acc = fmaf(-Ad[i][l], t[l], acc);
+        for (int l = 0; l < i; l += 4) {  // A is 0 on its diagonal block's diagonal and above
+          const float4 c = *reinterpret_cast<const float4*>(&Ad[i][l]);
+          acc = fmaf(-c.x, t[l], acc);
+          if (l + 1 < i) acc = fmaf(-c.y, t[l + 1], acc);
+          if (l + 2 < i) acc = fmaf(-c.z, t[l + 2], acc);
+          if (l + 3 < i) acc = fmaf(-c.w, t[l + 3], acc);
+        }
         t[i] = acc;
       }
       uint8_t* dst = s.m.T[tri(warp, warp)][0] + 2 * (col & 7);
@@ -395,7 +431,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
       }
       acc_terms(acc, ta);
 #pragma unroll
-      for (int u = 0; u < kTerms; ++u) put_left(s.m.T[tri(R, C)][u], ta[u]);
+      for (int u = 0; u < kTerms; ++u) put_left(s.m.T[tri(R, C)][u] + left, turn, ta[u]);
     }
     __syncthreads();
     // P T: five block products for each warp; T and P T leave
@@ -419,17 +455,18 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
         acc.add(pa[0], tb[0]);
       }
       // T: the warp's 32 pieces of a term are 512 contiguous bytes of the record
-      const int row = lane & 15, half = lane >> 4;
-      uint8_t* out = rec + row_piece(16 * (pi - pj) + row, 8 * half);
+      uint8_t* out = rec + row_piece(lane & 15, 8 * (lane >> 4)) + 512 * (pi - pj);
 #pragma unroll
       for (int u = 0; u < kTerms; ++u)
         *reinterpret_cast<uint4*>(out + term_base(u) + (u == 2 ? tri_base(pj) : pair_base(pj))) =
             *reinterpret_cast<const uint4*>(s.m.T[tri(pi, pj)][u] + piece);
+      // P T: rows 64 - 16 pj of the operand on, row 16 (pi - pj) + ... of them
+      uint8_t* o_at = rec + pair_base(pj) + 512 * (4 + pi - 2 * pj) + row_piece(r4, j2);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         uint32_t t[kOutTerms];
         split2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1], t);
-        uint8_t* o2 = rec + row_piece(64 + 16 * (pi - 2 * pj) + r4 + 8 * (z & 1), 8 * (z >> 1) + j2) + pair_base(pj);
+        uint8_t* o2 = o_at + row_piece(8 * (z & 1), 8 * (z >> 1));
         *reinterpret_cast<uint32_t*>(o2 + term_base(0)) = t[0];
         *reinterpret_cast<uint32_t*>(o2 + term_base(1)) = t[1];
       }
