@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int c = blockIdx.x / a.r.h_k, hk = blockIdx.x - c * a.r.h_k;
+  let_next_start();
   int first, n;
   if (!block_span(a, c, first, n)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

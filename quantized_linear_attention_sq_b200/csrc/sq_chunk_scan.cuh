@@ -236,7 +236,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int first, n;
   ragged_span(a, b, first, n);
-  if (n < a.min_long) return;
+  if (n < a.min_long) {
+    wait_for_previous();
+    return;
+  }
   const int slot = a.slots ? a.slots[b] : b;
   const int blocks = (n + 63) >> 6, c0 = args.p.cu_blocks[b];
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
@@ -244,6 +247,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     for (int x = tid; x < n * 16; x += kScanThreads)
       reinterpret_cast<uint4*>(out + ((size_t)(first + (x >> 4)) * a.h_v + h) * 128)[x & 15] = make_uint4(0, 0, 0, 0);
     if (tid == 0) atomicOr(a.t.status, ST_SLOT);
+    wait_for_previous();
     return;
   }
   const bool resume = a.past && a.past[b] > 0;
@@ -314,6 +318,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
       issued = i + 1;
     };
+    wait_for_previous();  // the prepared blocks
     load(0);
     if (blocks > 1) load(1);
     for (int i = 0; i < blocks; ++i) {
@@ -592,6 +597,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (ok && i + 1 < blocks) ok = take_rows(i + 1);
     }
   }
+  wait_for_previous();
   tc_before();
   __syncthreads();
   tc_after();

@@ -61,6 +61,24 @@ cudaError_t allow_smem(K kernel, int device, std::atomic<uint64_t>& seen) {
   return e;
 }
 
+// A launch that may overlap the end of the one before it on the stream (the
+// kernel itself waits where it must).
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), bool overlap, int64_t grid, int threads, size_t smem, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // ------------------------------------------------------------------- norms
 template <int D, typename TI, typename TO>
 void launch_norm(const sqr::NormArgs& a, int grid, cudaStream_t st) {
@@ -92,8 +110,8 @@ cudaError_t launch_rows(const sqr::RaggedArgs& a, const RowsLaunch& l) {
   if (e != cudaSuccess) return e;
   const size_t smem = sqr::RGeo<D>::smem(PACKED, a.rec_cap);
   const int64_t tiles = (int64_t)a.B * a.h_v, most = 2ll * l.sms * (128 / D) * (128 / D);
-  kern<<<(int)(tiles < most ? tiles : most), sqr::RGeo<D>::NT, smem, l.st>>>(a);
-  return cudaGetLastError();
+  // beside blocks (min_long), the launch before is the blocks' preparation
+  return launch(kern, a.min_long > 0, tiles < most ? tiles : most, sqr::RGeo<D>::NT, smem, l.st, a);
 }
 template <int D, bool KDA, typename T>
 cudaError_t launch_rows_pool(const sqr::RaggedArgs& a, const RowsLaunch& l) {
@@ -150,32 +168,40 @@ sq_status row_map(CUtensorMap* m, const char* name, const void* p, int64_t strid
   return r == CUDA_SUCCESS ? SQ_OK : fail(SQ_ERR_CUDA, "tensor map of %s: driver error %d", name, (int)r);
 }
 
-sq_status launch_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_ragged_tables& t, void* workspace,
-                        cudaStream_t st) {
+struct Blocks {
   sqr::ScanArgs a{};
-  a.p.r = r;
-  a.p.cu_blocks = t.cu_blocks;
-  a.p.block_req = t.block_req;
-  a.p.ws = static_cast<uint8_t*>(workspace);
-  a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
-  CUtensorMap qm, km, vm, om;
-  sq_status s = row_map(&qm, "q", r.q, r.q_stride, r.h_k, r.rows);
-  if (s == SQ_OK) s = row_map(&km, "k", r.k, r.k_stride, r.h_k, r.rows);
-  if (s == SQ_OK) s = row_map(&vm, "v", r.v, r.v_stride, r.h_v, r.rows);
-  if (s == SQ_OK) s = row_map(&om, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows);
+  CUtensorMap q, k, v, o;
+};
+
+// Sets up the blocks' arguments and launches their preparation.
+sq_status start_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_ragged_tables& t, void* workspace,
+                       cudaStream_t st, Blocks& b) {
+  b.a.p.r = r;
+  b.a.p.cu_blocks = t.cu_blocks;
+  b.a.p.block_req = t.block_req;
+  b.a.p.ws = static_cast<uint8_t*>(workspace);
+  b.a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
+  sq_status s = row_map(&b.q, "q", r.q, r.q_stride, r.h_k, r.rows);
+  if (s == SQ_OK) s = row_map(&b.k, "k", r.k, r.k_stride, r.h_k, r.rows);
+  if (s == SQ_OK) s = row_map(&b.v, "v", r.v, r.v_stride, r.h_v, r.rows);
+  if (s == SQ_OK) s = row_map(&b.o, "o", r.o, (int64_t)r.h_v * 128, r.h_v, r.rows);
   if (s != SQ_OK) return s;
-  static std::atomic<uint64_t> seen_prepare{0}, seen_fp32{0}, seen_packed{0};
-  auto scan = r.fmt_fp32 ? sqr::k_chunk_scan<false> : sqr::k_chunk_scan<true>;
-  cudaError_t e = allow_smem(sqr::k_chunk_prepare, h->device, seen_prepare);
-  if (e == cudaSuccess) e = allow_smem(scan, h->device, r.fmt_fp32 ? seen_fp32 : seen_packed);
-  if (e != cudaSuccess) return cuda_fail(e, "setting the block kernels' shared memory");
-  sqr::k_chunk_prepare<<<(unsigned)a.p.n_blocks * r.h_k, sqr::kPrepThreads, sizeof(sqr::PrepSmem), st>>>(a.p);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    scan<<<r.B * r.h_v, sqr::kScanThreads, sqr::kScanSmem, st>>>(qm, km, vm, om, a);
-    e = cudaGetLastError();
-  }
-  return e == cudaSuccess ? SQ_OK : cuda_fail(e, "launching the block kernels");
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = allow_smem(sqr::k_chunk_prepare, h->device, seen);
+  if (e == cudaSuccess)
+    e = launch(sqr::k_chunk_prepare, false, (int64_t)b.a.p.n_blocks * r.h_k, sqr::kPrepThreads, sizeof(sqr::PrepSmem),
+               st, b.a.p);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, "launching the blocks' preparation");
+}
+
+template <bool PACKED>
+sq_status finish_blocks(const sq_handle* h, const Blocks& b, cudaStream_t st) {
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = allow_smem(sqr::k_chunk_scan<PACKED>, h->device, seen);
+  if (e == cudaSuccess)
+    e = launch(sqr::k_chunk_scan<PACKED>, true, (int64_t)b.a.p.r.B * b.a.p.r.h_v, sqr::kScanThreads, sqr::kScanSmem, st,
+               b.q, b.k, b.v, b.o, b.a);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, "launching the blocks' scan");
 }
 
 }  // namespace
@@ -349,20 +375,28 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   a.wait_ns = h->wait_ns;
   a.t = h->tables;
   cudaStream_t st = as_stream(stream);
-  if (rows > 0 && in_blocks(h, dtype, max_len)) {
+  const bool blocks = rows > 0 && in_blocks(h, dtype, max_len);
+  Blocks bl;
+  if (blocks) {
     if (((int64_t)rows / SQ_RAGGED_BLOCK + B) * h->desc.h_k > (int64_t)INT32_MAX)
       return fail(SQ_ERR_UNSUPPORTED, "too many blocks of rows");
     a.min_long = kMinLong;
-    s = launch_blocks(h, a, *tables, workspace, st);
+    s = start_blocks(h, a, *tables, workspace, st, bl);
     if (s != SQ_OK) return s;
-    h->launches += 2;
+    h->launches++;
   }
+  // the short requests run beside the preparation of the long ones
   const RowsLaunch l{h->device, h->num_sms, st};
   if (d == 128) e = launch_rows_gate<128>(kda, dtype, a, l);
   else if (d == 64) e = launch_rows_gate<64>(kda, dtype, a, l);
   else e = launch_rows_gate<32>(kda, dtype, a, l);
   if (e != cudaSuccess) return cuda_fail(e, "launching the ragged rows");
   h->launches++;
+  if (blocks) {
+    s = a.fmt_fp32 ? finish_blocks<false>(h, bl, st) : finish_blocks<true>(h, bl, st);
+    if (s != SQ_OK) return s;
+    h->launches++;
+  }
   return SQ_OK;
 }
 

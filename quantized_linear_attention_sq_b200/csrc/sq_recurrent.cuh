@@ -48,6 +48,14 @@ struct RaggedArgs {
   Tables t;
 };
 
+// Launches that overlap (programmatic dependence): a kernel lets the next one
+// of its call start as soon as all its own CTAs have, and waits for the one
+// before it to be over where it needs its results, and before it ends, so
+// that the end of a call is the end of all its kernels. Without effect in a
+// plain launch.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Request b's rows, cut to the arrays.
 __device__ __forceinline__ void ragged_span(const RaggedArgs& a, int b, int& first, int& n) {
   first = min(max(a.cu_seqlens[b], 0), a.rows);
@@ -303,6 +311,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
     sqk::cp_async_commit();
   };
 
+  let_next_start();
   if (tid == 0) {
     sqk::mbar_init(&arrived, 1);
     sqk::fence_mbar_init();
@@ -458,6 +467,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   __syncthreads();  // the rows' vectors and the staged state have been read
   }
   if (st) atomicOr(a.t.status, st);
+  wait_for_previous();
 }
 
 }  // namespace sqr
