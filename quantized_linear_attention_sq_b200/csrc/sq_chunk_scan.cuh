@@ -358,9 +358,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const uint64_t qt = smem_desc(stage, 16, 1024, 2), kt = qt + kTileBytes / 32;
       if (!warp_wait(ctl, &ctl.full[i & 1], (i >> 1) & 1, ns)) break;
       bool ok = true;
-#pragma unroll 1
-      for (int y = 0; y < 2 && ok; ++y) {  // k: the key rows 64 y .. 64 y + 63
-        ok = warp_wait(ctl, &ctl.s_ready[y], ph, ns);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {  // k: the key rows 64 y .. 64 y + 63
+        ok = ok && warp_wait(ctl, &ctl.s_ready[y], ph, ns);
         tc_after();
         if (ok && elect_one()) {
 #pragma unroll
@@ -490,6 +490,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const int live = min(64, n - 64 * i);
       const float* coef = reinterpret_cast<const float*>(smem + (i & 1) * kStageBytes + kStagePrep + kTermsBytes);
       uint32_t w[2][8];
+      auto factors = [&](float2 (&e)[2], int from) {  // of this lane's rows, read before a wait
+        e[0] = *reinterpret_cast<const float2*>(coef + from + j2);
+        e[1] = *reinterpret_cast<const float2*>(coef + from + j2 + 8);
+      };
+      float2 e[2];
+      factors(e, 128);
       if (!warp_wait(ctl, &ctl.d1, ph, ns)) break;
       tc_after();
       tc_ld_frag(w[0], tl + TM_D1K + 16 * part);
@@ -498,21 +504,22 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       tc_wait_ld(w[1]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float2 e = *reinterpret_cast<const float2*>(coef + 128 + j2 + 8 * g);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           float* y = &x[m >> 1][4 * g + 2 * (m & 1)];
-          y[0] = fmaf(-e.x, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]), y[0]);
-          y[1] = fmaf(-e.y, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]), y[1]);
-          if (live < 64) {  // whatever the rows behind the last held
-            if (j2 + 8 * g >= live) y[0] = 0.0f;
-            if (j2 + 8 * g + 1 >= live) y[1] = 0.0f;
-          }
+          y[0] = fmaf(-e[g].x, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]), y[0]);
+          y[1] = fmaf(-e[g].y, __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]), y[1]);
         }
+      }
+      if (live < 64) {  // whatever the rows behind the last held
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+          if (j2 + 8 * ((z >> 2) & 1) + (z & 1) >= live) x[z >> 3][z & 7] = 0.0f;
       }
       put_frag(x, rt, rt + 32, rt + 64);
       warp_arrive(&ctl.r_ready);
 
+      factors(e, 192);
       if (!warp_wait(ctl, &ctl.d2, ph, ns)) break;
       tc_after();
       tc_ld_frag(w[0], tl + TM_D2 + 16 * part);
@@ -521,17 +528,17 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       tc_wait_ld(w[1]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float2 e = *reinterpret_cast<const float2*>(coef + 192 + j2 + 8 * g);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          x[m >> 1][4 * g + 2 * (m & 1)] = e.x * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]);
-          x[m >> 1][4 * g + 2 * (m & 1) + 1] = e.y * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]);
+          x[m >> 1][4 * g + 2 * (m & 1)] = e[g].x * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1)]);
+          x[m >> 1][4 * g + 2 * (m & 1) + 1] = e[g].y * __uint_as_float(w[m >> 1][4 * g + 2 * (m & 1) + 1]);
         }
       }
       put_frag(x, ut + u_col(0), ut + u_col(1), ut + u_col(2));
       warp_arrive(&ctl.u_ready);
 
       // o, under the state's product
+      factors(e, 0);
       if (!warp_wait(ctl, &ctl.d2o, ph, ns)) break;
       if (i > 0 && !warp_wait(ctl, &ctl.o_free, (i - 1) & 1, ns)) break;
       {
@@ -549,12 +556,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         __nv_bfloat162 bad = __float2bfloat162_rn(0.0f);  // stays 0 while every o is finite
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float2 e = *reinterpret_cast<const float2*>(coef + j2 + 8 * g);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int z = 4 * g + 2 * (m & 1);
-            o[g][m] = bf16x2(fmaf(e.x, __uint_as_float(w[m >> 1][z]), __uint_as_float(y[m >> 1][z])),
-                             fmaf(e.y, __uint_as_float(w[m >> 1][z + 1]), __uint_as_float(y[m >> 1][z + 1])));
+            o[g][m] = bf16x2(fmaf(e[g].x, __uint_as_float(w[m >> 1][z]), __uint_as_float(y[m >> 1][z])),
+                             fmaf(e[g].y, __uint_as_float(w[m >> 1][z + 1]), __uint_as_float(y[m >> 1][z + 1])));
             bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&o[g][m]), __float2bfloat162_rn(0.0f), bad);
           }
           stmatrix4t(smem + kOutAt + at + 1024 * g, o[g][0], o[g][1], o[g][2], o[g][3]);
