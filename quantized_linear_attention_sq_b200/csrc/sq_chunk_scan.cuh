@@ -52,7 +52,7 @@ struct ScanCtl {
   uint64_t s_ready[2], d3[2];
   uint64_t r_ready, u_ready, d1, d2, d2o, o_ready, o_free, drain;
   uint32_t tmem;
-  int32_t abort;
+  int32_t abort, request;
 };
 constexpr size_t kScanSmem = 1024 + kOutAt + kTileBytes + sizeof(ScanCtl) + 16;
 
@@ -223,6 +223,34 @@ __device__ __forceinline__ bool warp_wait(ScanCtl& c, uint64_t* bar, uint32_t pa
 // The 256 threads of the record's thread map.
 __device__ __forceinline__ void record_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// The request whose turn it is as the `rank`-th: of up to kRanked requests the
+// longest start first, so that no long one is left to run alone (24 requests
+// of 0..1900 rows: 146 us in their own order, 113 by length); with more
+// the order matters little and the search would take long.
+constexpr int kRanked = 256;
+__device__ __forceinline__ int request_of(const RaggedArgs& a, int rank, int32_t* length, int32_t* found) {
+  if (a.B > kRanked || a.B == 1) return rank;
+  const int tid = threadIdx.x, padded = (a.B + 3) & ~3;
+  int n = -1;
+  if (tid < a.B) {
+    int first;
+    ragged_span(a, tid, first, n);
+  }
+  if (tid < padded) length[tid] = n;
+  __syncthreads();
+  if (tid < a.B) {
+    int before = 0;
+    for (int j = 0; j < padded; j += 4) {
+      const int4 l = *reinterpret_cast<const int4*>(length + j);
+      before += (l.x > n || (l.x == n && j < tid)) + (l.y > n || (l.y == n && j + 1 < tid)) +
+                (l.z > n || (l.z == n && j + 2 < tid)) + (l.w > n || (l.w == n && j + 3 < tid));
+    }
+    if (before == rank) *found = tid;
+  }
+  __syncthreads();
+  return *found;
+}
+
 template <bool PACKED>
 __global__ void __launch_bounds__(kScanThreads, 1)
     k_chunk_scan(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -232,8 +260,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   ScanCtl& ctl = *reinterpret_cast<ScanCtl*>(smem + kOutAt + kTileBytes);
   const RaggedArgs& a = args.p.r;
-  const int b = blockIdx.x / a.h_v, h = blockIdx.x - b * a.h_v, hk = h / (a.h_v / a.h_k);
+  const int rank = blockIdx.x / a.h_v, h = blockIdx.x - rank * a.h_v, hk = h / (a.h_v / a.h_k);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = request_of(a, rank, reinterpret_cast<int32_t*>(smem), &ctl.request);
   int first, n;
   ragged_span(a, b, first, n);
   if (n < a.min_long) {
