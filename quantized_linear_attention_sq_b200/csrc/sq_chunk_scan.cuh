@@ -263,14 +263,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int rank = blockIdx.x / a.h_v, h = blockIdx.x - rank * a.h_v, hk = h / (a.h_v / a.h_k);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = request_of(a, rank, reinterpret_cast<int32_t*>(smem), &ctl.request);
+  // everything about the request at once: its loads wait on none of each other
+  const int slot = a.slots ? a.slots[b] : b, c0 = args.p.cu_blocks[b];
+  const bool resume = a.past && a.past[b] > 0;
   int first, n;
   ragged_span(a, b, first, n);
   if (n < a.min_long) {
     wait_for_previous();
     return;
   }
-  const int slot = a.slots ? a.slots[b] : b;
-  const int blocks = (n + 63) >> 6, c0 = args.p.cu_blocks[b];
+  const int blocks = (n + 63) >> 6;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
   if (slot < 0 || slot >= a.n_slots || c0 < 0 || c0 + blocks > args.p.n_blocks) {
     for (int x = tid; x < n * 16; x += kScanThreads)
@@ -279,7 +281,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     wait_for_previous();
     return;
   }
-  const bool resume = a.past && a.past[b] > 0;
   uint8_t* record = a.pool + (uint64_t)slot * a.slot_bytes + (PACKED ? a.t.rec_off[h] : 0u);
   float* S_pool = reinterpret_cast<float*>(a.pool) + ((size_t)slot * a.h_v + h) * 128 * 128;
 
@@ -312,7 +313,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int part = warp >> 2, col = (warp & 3) * 32 + lane;  // compute warps
   float S[2][16];
   if (PACKED && resume) {
-    if (warp < 8) unpack_state<128>(a, h, record, smem + 128 * 128 * 4, reinterpret_cast<float*>(smem), record_sync);
+    uint8_t* rec = smem + 128 * 128 * 4;
+    if (warp < 8) {
+      for (uint32_t x = tid * 16; x < a.t.rec_bytes[h]; x += 256 * 16) cp_async16(rec + x, record + x);
+      sqk::cp_async_commit();
+      RecordMap<128> m;
+      map_record<128>(a, h, m);
+      cp_async_wait_all_groups();
+      record_sync();
+      unpack_record<128>(m, rec, reinterpret_cast<float*>(smem));
+    }
     __syncthreads();
   }
   if (warp < kMoveWarp) {
@@ -648,6 +658,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     for (int x = 0; x < 32; ++x) dst[(64 * (x >> 4) + (x & 15)) * 128] = S[x >> 4][x & 15];
   }
   if (PACKED) {
+    if (warp < 8) {
+      fetch_pack_tables<128>(a, h, smem + 128 * 128 * 4);
+      cp_async_wait_all_groups();
+    }
     __syncthreads();
     if (warp < 8) st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, reinterpret_cast<float*>(smem), record_sync);
   }

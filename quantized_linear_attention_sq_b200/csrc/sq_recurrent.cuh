@@ -100,6 +100,7 @@ __device__ __forceinline__ float4 load4(const __half* p) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sqk::smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all_groups() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // One row's vectors in shared memory, as they came: k, q, v, then (fp32) the
@@ -138,42 +139,64 @@ struct RowTile {
 };
 enum { TILE_END = 0, TILE_RUN = 1, TILE_RESUME = 2, TILE_ZERO = 4 };  // RUN: store a state; ZERO: a bad slot, o = 0
 
-// A packed record in shared memory, dequantized into S [D][D] there.
-// `sync`: a barrier of the Geo<D>::NT threads that call it.
-template <int D, typename Sync>
-__device__ __forceinline__ void unpack_record(const RaggedArgs& a, int h, const uint8_t* rec, float* S, Sync sync) {
+// A head's row tables and column scales as a thread of the record's thread map
+// needs them to dequantize, read before the record is there.
+template <int D>
+struct RecordMap {
+  uint32_t row[Geo<D>::RPT];  // offset of the row's codes, its width above
+  float4 col[4];
+};
+template <int D>
+__device__ __forceinline__ void map_record(const RaggedArgs& a, int h, RecordMap<D>& m) {
   using G = Geo<D>;
   static_assert(G::NT == RGeo<D>::NT, "one thread map");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cc = lane % G::LPR, rg = warp * G::RPW + lane / G::LPR;
-  const float* col = a.t.col + (size_t)h * D + 16 * cc;
+  const int lane = threadIdx.x & 31, cc = lane % G::LPR, rg = (threadIdx.x >> 5) * G::RPW + lane / G::LPR;
+#pragma unroll
+  for (int r = 0; r < G::RPT; ++r)
+    m.row[r] = a.t.row_off[(size_t)h * D + r * G::NG + rg] | (uint32_t)a.t.row_code[(size_t)h * D + r * G::NG + rg] << 16;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) m.col[p] = *reinterpret_cast<const float4*>(a.t.col + (size_t)h * D + 16 * cc + 4 * p);
+}
+// A packed record in shared memory, dequantized into S [D][D] there.
+template <int D>
+__device__ __forceinline__ void unpack_record(const RecordMap<D>& m, const uint8_t* rec, float* S) {
+  using G = Geo<D>;
+  const int lane = threadIdx.x & 31, cc = lane % G::LPR, rg = (threadIdx.x >> 5) * G::RPW + lane / G::LPR;
 #pragma unroll
   for (int r = 0; r < G::RPT; ++r) {
     const int i = r * G::NG + rg;
-    const uint8_t code = a.t.row_code[(size_t)h * D + i];
+    const uint8_t code = (uint8_t)(m.row[r] >> 16);
     const float mul = code == ROW_PIVOT ? 1.0f : __half2float(reinterpret_cast<const __half*>(rec)[i]);
     float2 T[8];
-    sqk::load_row(rec + a.t.row_off[(size_t)h * D + i], code, cc, mul, T);
+    sqk::load_row(rec + (m.row[r] & 0xffffu), code, cc, mul, T);
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-      reinterpret_cast<float2*>(S + (size_t)i * D + 16 * cc)[p] =
-          __fmul2_rn(T[p], make_float2(col[2 * p], col[2 * p + 1]));
+    for (int p = 0; p < 4; ++p) {
+      const float2 lo = __fmul2_rn(T[2 * p], make_float2(m.col[p].x, m.col[p].y));
+      const float2 hi = __fmul2_rn(T[2 * p + 1], make_float2(m.col[p].z, m.col[p].w));
+      reinterpret_cast<float4*>(S + (size_t)i * D + 16 * cc)[p] = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
   }
-  sync();
-}
-// The same from the pool, through `rec`.
-template <int D, typename Sync>
-__device__ __forceinline__ void unpack_state(const RaggedArgs& a, int h, const uint8_t* src, uint8_t* rec, float* S,
-                                             Sync sync) {
-  const uint32_t rb = a.t.rec_bytes[h];
-  for (uint32_t x = threadIdx.x * 16; x < rb; x += Geo<D>::NT * 16)
-    *reinterpret_cast<uint4*>(rec + x) = *reinterpret_cast<const uint4*>(src + x);
-  sync();
-  unpack_record<D>(a, h, rec, S, sync);
 }
 
-// S [D][D] in shared memory, quantized into the slot's record
-// (the quantization of sq_quantize_state). Returns status bits.
+// The head's tables that the quantization reads: D row impacts, row offsets,
+// row widths (7 D bytes behind the record), on their way to shared memory.
+template <int D>
+__device__ __forceinline__ uint8_t* pack_tables(uint8_t* rec, uint32_t rb) { return rec + (rb + 15) / 16 * 16; }
+template <int D>
+__device__ __forceinline__ void fetch_pack_tables(const RaggedArgs& a, int h, uint8_t* rec) {
+  uint8_t* t = pack_tables<D>(rec, a.t.rec_bytes[h]);
+  for (int x = threadIdx.x; x < 7 * D / 4; x += Geo<D>::NT) {
+    const uint8_t* src = x < D ? reinterpret_cast<const uint8_t*>(a.t.phi + (size_t)h * D + x)
+                         : x < D + D / 2 ? reinterpret_cast<const uint8_t*>(a.t.row_off + (size_t)h * D) + 4 * (x - D)
+                                         : a.t.row_code + (size_t)h * D + 4 * (x - D - D / 2);
+    sqk::cp_async4(t + 4 * x, src);
+  }
+  sqk::cp_async_commit();
+}
+// S [D][D] in shared memory, quantized into the slot's record (the
+// quantization of sq_quantize_state), with the tables of fetch_pack_tables
+// behind `rec`. `sync`: a barrier of the Geo<D>::NT threads that call it;
+// one has passed since S and the tables were complete. Returns status bits.
 template <int D, typename Sync>
 __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8_t* dst, uint8_t* rec, const float* S,
                                                Sync sync) {
@@ -181,24 +204,23 @@ __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cc = lane % G::LPR, rg = warp * G::RPW + lane / G::LPR;
   const uint32_t rb = a.t.rec_bytes[h];
-  float* phi = reinterpret_cast<float*>(rec + (rb + 15) / 16 * 16);
-  uint16_t* row_off = reinterpret_cast<uint16_t*>(phi + D);
-  uint8_t* row_code = reinterpret_cast<uint8_t*>(row_off + D);
-  for (int i = tid; i < D; i += G::NT) {
-    row_off[i] = a.t.row_off[(size_t)h * D + i];
-    row_code[i] = a.t.row_code[(size_t)h * D + i];
-    phi[i] = a.t.phi[(size_t)h * D + i];
-  }
-  for (uint32_t x = tid * 16; x < rb; x += G::NT * 16) *reinterpret_cast<uint4*>(rec + x) = make_uint4(0, 0, 0, 0);
-  sync();  // the tables, the cleared record, and S
-  const float* icol = a.t.icol + (size_t)h * D + 16 * cc;
+  const float* phi = reinterpret_cast<const float*>(pack_tables<D>(rec, rb));
+  const uint16_t* row_off = reinterpret_cast<const uint16_t*>(phi + D);
+  const uint8_t* row_code = reinterpret_cast<const uint8_t*>(row_off + D);
+  float4 icol[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) icol[p] = *reinterpret_cast<const float4*>(a.t.icol + (size_t)h * D + 16 * cc + 4 * p);
+  if (tid < 1) *reinterpret_cast<uint4*>(rec + rb - 16) = make_uint4(0, 0, 0, 0);  // the padding's bytes
+  sync();
   float2 T[G::RPT][8];
 #pragma unroll
   for (int r = 0; r < G::RPT; ++r)
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-      T[r][p] = __fmul2_rn(reinterpret_cast<const float2*>(S + (size_t)(r * G::NG + rg) * D + 16 * cc)[p],
-                           make_float2(icol[2 * p], icol[2 * p + 1]));
+    for (int p = 0; p < 4; ++p) {
+      const float4 x = reinterpret_cast<const float4*>(S + (size_t)(r * G::NG + rg) * D + 16 * cc)[p];
+      T[r][2 * p] = __fmul2_rn(make_float2(x.x, x.y), make_float2(icol[p].x, icol[p].y));
+      T[r][2 * p + 1] = __fmul2_rn(make_float2(x.z, x.w), make_float2(icol[p].z, icol[p].w));
+    }
   const uint32_t st = sqk::requant_rows<D, 0>(rec, row_off, row_code, phi, rg, cc, false, T);
   sync();
   for (uint32_t x = tid * 16; x < rb; x += G::NT * 16)
@@ -340,11 +362,20 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   const bool resume = c.what & TILE_RESUME;
   float4 S[R::RPT];
   bool ok = true;
-  if (resume) {
+  if (PACKED) {
+    uint8_t* rec_out = rec_in + (a.rec_cap + 127) / 128 * 128;
+    if (resume) {
+      RecordMap<D> m;
+      map_record<D>(a, c.h, m);
+      ok = sqk::mbar_wait_bounded(&arrived, phase & 1, a.wait_ns);
+      if (ok) unpack_record<D>(m, rec_in, Ssh);
+    }
+    if (c.what & TILE_RUN) fetch_pack_tables<D>(a, c.h, rec_out);
+    __syncthreads();
+  } else if (resume) {
     ok = sqk::mbar_wait_bounded(&arrived, phase & 1, a.wait_ns);
-    ++phase;
-    if (PACKED && ok) unpack_record<D>(a, c.h, rec_in, Ssh, [] { __syncthreads(); });
   }
+  if (resume) ++phase;
 #pragma unroll
   for (int r = 0; r < R::RPT; ++r)
     S[r] = resume && ok ? *reinterpret_cast<const float4*>(Ssh + (row0 + r) * D + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -457,7 +488,9 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
 #pragma unroll
       for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r) * D + c4) = S[r];
       uint8_t* rec_out = rec_in + (a.rec_cap + 127) / 128 * 128;
-      st |= pack_state<D>(a, c.h, record_of(c), rec_out, Ssh, [] { __syncthreads(); });  // its first barrier orders S
+      cp_async_wait_all_groups();  // the tables (and the next rows)
+      __syncthreads();
+      st |= pack_state<D>(a, c.h, record_of(c), rec_out, Ssh, [] { __syncthreads(); });
     } else {
       float* S_pool = state_of(c);
 #pragma unroll
