@@ -31,7 +31,8 @@ typedef enum { SQ_F32 = 0, SQ_BF16 = 1, SQ_F16 = 2 } sq_dtype;
 /* Rows of one block of the block tables. */
 #define SQ_RAGGED_BLOCK 64
 
-/* Most requests of one ragged batch. */
+/* Most requests of one ragged batch (and at most 2^30 rows or slots):
+ * SQ_ERR_UNSUPPORTED beyond. */
 #define SQ_RAGGED_MAX_REQUESTS 16384
 
 /* Further bits of the status word. */
@@ -125,7 +126,8 @@ typedef struct {
  *   g        device fp32 [rows, h_v] (SQ_GATE_HEAD) or [rows, h_v, d]
  *            (SQ_GATE_KEY_CHANNEL, then 16-byte aligned), in [0, 1]; values
  *            outside are taken as the nearer bound
- *   o        device, type `dtype`, contiguous [rows, h_v, d]; rows of no request are left as they were
+ *   o        device, type `dtype`, contiguous [rows, h_v, d]; rows of no
+ *            request are left as they were; must not overlap an input
  *   slot_ids device int32 [B] (distinct), or NULL for slots 0..B-1; a
  *            request whose slot is out of range gets o = 0 and
  *            SQ_STATUS_BAD_SLOT, and no state
@@ -135,10 +137,12 @@ typedef struct {
  *   workspace  device, 16-byte aligned, sq_ragged_workspace_bytes() bytes,
  *            used by this call's kernels only while they run: calls that may
  *            overlap (two streams, two graphs in flight) need one each
- * SQ_BF16 rows of SQ_GATE_HEAD pools with d = 128 run in blocks of 64 rows on
- * the tensor cores (fp32-accurate: operands are split into bf16 terms);
- * other requests run row by row in fp32. NaN or infinity in a row reaches o
- * from its block of 64 rows on, and no other request. */
+ * SQ_BF16 requests of SQ_GATE_HEAD pools with d = 128 that are not very short
+ * run in blocks of 64 rows on the tensor cores: the state stays accurate to
+ * fp32 (operands are split into bf16 terms), so it differs from a row by row
+ * run in its last bits only. All others run row by row in fp32. A NaN or an
+ * infinity in a row reaches the state and o from its block of 64 rows on, and
+ * no other request. */
 sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void* k, const void* v, int64_t q_row_stride,
                             int64_t k_row_stride, int64_t v_row_stride, int32_t dtype, const float* beta,
                             const float* g, void* o, const sq_ragged_tables* tables, const int32_t* slot_ids, int32_t B,

@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     for (int x = 0; x < 32; ++x) S[x >> 4][x & 15] = resume ? src[(64 * (x >> 4) + (x & 15)) * 128] : 0.0f;
     if (PACKED && resume) sqk::fence_proxy_async_smem();  // before TMA writes where S was read
   }
+  wait_for_previous();  // the prepared blocks; before the first wait with a limit
   tc_before();
   __syncthreads();
   tc_after();
@@ -357,7 +358,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
       issued = i + 1;
     };
-    wait_for_previous();  // the prepared blocks
     load(0);
     if (blocks > 1) load(1);
     for (int i = 0; i < blocks; ++i) {
@@ -642,7 +642,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (ok && i + 1 < blocks) ok = take_rows(i + 1);
     }
   }
-  wait_for_previous();
   tc_before();
   __syncthreads();
   tc_after();

@@ -23,6 +23,8 @@ namespace {
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Most rows of a call: row numbers and their steps stay within 32 bits.
+constexpr int32_t kMaxRows = 1 << 30;
 inline int elt_bytes(int dtype) { return dtype == SQ_F32 ? 4 : 2; }
 
 #define SQ_NEED(p, n)                                                                       \
@@ -217,6 +219,8 @@ sq_status sq_batch_tables(const int32_t* lengths, const int32_t* past, int32_t B
     return fail(SQ_ERR_INVALID_ARG, "B, max_rows and n_slots must be >= 0 (got %d, %d, %d)", B, max_rows, n_slots);
   if (B > SQ_RAGGED_MAX_REQUESTS)
     return fail(SQ_ERR_UNSUPPORTED, "B = %d is above %d requests", B, SQ_RAGGED_MAX_REQUESTS);
+  if (max_rows > kMaxRows || n_slots > kMaxRows)
+    return fail(SQ_ERR_UNSUPPORTED, "max_rows = %d or n_slots = %d is above %d", max_rows, n_slots, kMaxRows);
   SQ_NEED(cu_seqlens, 4);
   SQ_NEED(cu_blocks, 4);
   if (B > 0) {
@@ -262,6 +266,7 @@ sq_status sq_qk_norm(const sq_norm_desc* desc, const void* q, const void* k, int
   if (d != 32 && d != 64 && d != 128) return fail(SQ_ERR_UNSUPPORTED, "d must be 32, 64 or 128 (got %d)", d);
   if (rows < 0 || h_q < 0 || h_k < 0)
     return fail(SQ_ERR_INVALID_ARG, "rows, h_q and h_k must be >= 0 (got %d, %d, %d)", rows, h_q, h_k);
+  if (rows > kMaxRows) return fail(SQ_ERR_UNSUPPORTED, "rows = %d is above %d", rows, kMaxRows);
   if ((int64_t)h_q + h_k > 65536) return fail(SQ_ERR_INVALID_ARG, "too many heads (%d + %d)", h_q, h_k);
   if (desc->rot_dim < 0 || desc->rot_dim > d || desc->rot_dim % 2 != 0)
     return fail(SQ_ERR_INVALID_ARG, "rot_dim = %d is not even in [0, %d]", desc->rot_dim, d);
@@ -317,6 +322,7 @@ sq_status sq_ragged_workspace_bytes(const sq_handle* h, int32_t dtype, int32_t B
   if (dtype < SQ_F32 || dtype > SQ_F16) return fail(SQ_ERR_INVALID_ARG, "bad element type %d", dtype);
   if (B < 0 || rows < 0 || max_len < 0)
     return fail(SQ_ERR_INVALID_ARG, "B, rows and max_len must be >= 0 (got %d, %d, %d)", B, rows, max_len);
+  if (rows > kMaxRows) return fail(SQ_ERR_UNSUPPORTED, "rows = %d is above %d", rows, kMaxRows);
   *bytes = in_blocks(h, dtype, max_len)
                ? (uint64_t)(rows / SQ_RAGGED_BLOCK + B) * (uint64_t)h->desc.h_v * sqr::kPrepBytes : 0;
   return SQ_OK;

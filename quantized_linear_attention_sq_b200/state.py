@@ -238,10 +238,11 @@ class StatePool:
                 return self.prefill_ragged(pool, q, k, v, beta, g, o, tables, slot_ids, max_len, workspace, stream)
         if workspace is None:
             need = self.ragged_workspace_bytes(B, rows, max_len, q.dtype)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-                if isinstance(stream, torch.cuda.Stream):
-                    workspace.record_stream(stream)
+            if need:  # allocated on the stream that uses it
+                on = (torch.cuda.current_stream() if stream is None else
+                      torch.cuda.ExternalStream(_raw_stream(stream, dev), device=self.device))
+                with torch.cuda.stream(on):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         i32 = torch.int32
         t = _abi.RaggedTables(_ptr(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
                               _ptr(tables.cu_blocks, i32, "cu_blocks", B + 1),

@@ -329,6 +329,94 @@ def test_ragged_packed_is_the_fp32_run_quantized(d, channel):
         a.close()
 
 
+def test_ragged_more_requests_than_are_ranked():
+    """Requests past the count up to which the longest start first, most of them short."""
+    lengths = [(b * 7) % 5 for b in range(300)]
+    lengths[3], lengths[150], lengths[299] = 90, 130, 64
+    bt = Batch(lengths, hv=2, hk=1)
+    try:
+        check_rows(bt.run())
+    finally:
+        bt.close()
+
+
+@pytest.mark.parametrize("n", [255, 256])
+def test_ragged_ranked_requests(n):
+    lengths = [10 + (b * 37) % 23 for b in range(n)]
+    bt = Batch(lengths, hv=1, hk=1)
+    try:
+        check_rows(bt.run())
+    finally:
+        bt.close()
+
+
+def test_ragged_longer_than_max_len():
+    """max_len chooses the kernels; a request that passes it is still right."""
+    for max_len in (1, 9, 10, 40):
+        bt = Batch([1, 77, 0, 200, 9], max_len=max_len)
+        try:
+            check_rows(bt.run())
+        finally:
+            bt.close()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_ragged_on_another_stream(packed):
+    """A call on a side stream, with the workspace that the call allocates."""
+    bt = Batch([100, 3, 64, 1], packed=packed)
+    try:
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        bt.run(stream=side)
+        first = bt.o.clone(), bt.pool.clone()
+        bt.pool.copy_(bt.packed0 if packed else bt.S0)
+        torch.cuda.synchronize()
+        bt.run(stream=side.cuda_stream)
+        assert torch.equal(first[0], bt.o) and torch.equal(first[1], bt.pool)
+        if not packed:
+            check_rows(bt)
+    finally:
+        bt.close()
+
+
+def test_ragged_nan_gate_and_beta():
+    for name in ("g", "beta"):
+        bt = Batch([100, 40, 3], past=[0, 0, 0])
+        try:
+            getattr(bt, name)[90, 1] = float("nan")   # request 0, row 90, head 1
+            bt.run()
+            check_rows(bt, skip=(0,))
+            want, S = bt.expected()[0]
+            assert rel(bt.o[:64].transpose(0, 1), want[:64].transpose(0, 1)) <= 2.0 ** -8 + 32 * U * 10
+            others = [0, 2, 3]
+            assert rel(bt.pool[bt.slots[0]][others], S[others]) <= 8 * U * math.sqrt(101)
+            assert bt.pool[bt.slots[0]][1].isnan().any()
+            assert bt.h.get_status() & _abi.SQ_STATUS_NAN
+        finally:
+            bt.close()
+
+
+def test_ragged_guard_bytes_around_every_output():
+    """o and the pool lie between guard regions that no call touches."""
+    pad = 1024
+    for packed, lengths in ((False, [130, 1, 65]), (True, [70, 0, 9, 129])):
+        bt = Batch(lengths, packed=packed, extra=0)
+        try:
+            o = torch.full((bt.o.numel() + 2 * pad,), 5.0, device="cuda", dtype=bt.o.dtype)
+            pool = torch.full((bt.pool.numel() + 2 * pad,), 5, device="cuda", dtype=bt.pool.dtype)
+            pool[pad:-pad] = bt.pool.flatten()
+            bt.h.prefill_ragged(pool[pad:-pad], bt.q, bt.k, bt.v, bt.beta, bt.g, o[pad:-pad], bt.tables,
+                                slot_ids=bt.slot_ids)
+            torch.cuda.synchronize()
+            for x in (o, pool):
+                assert (x[:pad] == 5).all() and (x[-pad:] == 5).all()
+            bt.run()
+            assert torch.equal(o[pad:-pad].view_as(bt.o), bt.o)
+            assert torch.equal(pool[pad:-pad].view_as(bt.pool), bt.pool)
+        finally:
+            bt.close()
+
+
 def test_ragged_gates_at_and_past_their_bounds():
     def gates(g):
         g[3::7] = 0.0

@@ -31,6 +31,8 @@ def _tables(L, **kw):
     (dict(rows=-1), _abi.SQ_ERR_INVALID_ARG, "B, max_rows"),
     (dict(n_slots=-2), _abi.SQ_ERR_INVALID_ARG, "n_slots"),
     (dict(B=_abi.SQ_RAGGED_MAX_REQUESTS + 1), _abi.SQ_ERR_UNSUPPORTED, "requests"),
+    (dict(rows=(1 << 30) + 1), _abi.SQ_ERR_UNSUPPORTED, "max_rows"),
+    (dict(n_slots=(1 << 30) + 1), _abi.SQ_ERR_UNSUPPORTED, "n_slots"),
     (dict(lengths=None), _abi.SQ_ERR_INVALID_ARG, "lengths is NULL"),
     (dict(lengths=A + 2), _abi.SQ_ERR_INVALID_ARG, "lengths is not"),
     (dict(cu=None), _abi.SQ_ERR_INVALID_ARG, "cu_seqlens"),
@@ -68,6 +70,7 @@ def _norm(L, desc=None, **kw):
     ({}, dict(tout=-1), _abi.SQ_ERR_INVALID_ARG, "element type"),
     ({}, dict(d=96), _abi.SQ_ERR_UNSUPPORTED, "d must be"),
     ({}, dict(rows=-1), _abi.SQ_ERR_INVALID_ARG, "rows"),
+    ({}, dict(rows=(1 << 30) + 1), _abi.SQ_ERR_UNSUPPORTED, "rows"),
     ({}, dict(q=None), _abi.SQ_ERR_INVALID_ARG, "q is NULL"),
     ({}, dict(q=A + 8), _abi.SQ_ERR_INVALID_ARG, "q is not 16-byte"),
     ({}, dict(qs=500), _abi.SQ_ERR_INVALID_ARG, "below"),
