@@ -23,7 +23,8 @@ def _arg(t, dtype, name, numel, dev):
     """Address of a contiguous tensor on CUDA device `dev` (None passes)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.get_device() == dev and t.is_contiguous() and numel in (None, t.numel()):
+    # get_device() is -1 for a CPU tensor
+    if t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and (numel is None or t.numel() == numel):
         return t.data_ptr()
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on device {dev}, not on {t.device}")
@@ -35,9 +36,10 @@ def _arg(t, dtype, name, numel, dev):
 
 
 def _device_of(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids=None, slot_used=None,

@@ -65,8 +65,8 @@ def row_ptr(t: torch.Tensor, dtype, name, rows, heads, d, dev: int):
     """(address, row stride in elements) of a [rows, heads, d] tensor whose
     rows may lie apart (a column slice of a wider matrix)."""
     shape, st = t.shape, t.stride()
-    if (t.dtype is dtype and t.is_cuda and t.get_device() == dev and len(shape) == 3 and shape[0] == rows
-            and shape[1] == heads and shape[2] == d and st[2] == 1 and (st[1] == d or heads == 1)):
+    if (t.get_device() == dev and t.dtype is dtype and shape == (rows, heads, d) and st[2] == 1
+            and (st[1] == d or heads == 1)):
         return t.data_ptr(), st[0] if rows > 1 else heads * d
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on device {dev}, not on {t.device}")
