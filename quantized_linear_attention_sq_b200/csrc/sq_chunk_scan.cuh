@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       cp_async_wait_all_groups();
     }
     __syncthreads();
-    if (warp < 8) st |= pack_state<128>(a, h, record, smem + 128 * 128 * 4, reinterpret_cast<float*>(smem), record_sync);
+    if (warp < 8) st |= pack_state<128>(a, h, record, reinterpret_cast<float*>(smem), smem + 128 * 128 * 4, record_sync);
   }
   if (st) atomicOr(a.t.status, st);
 }

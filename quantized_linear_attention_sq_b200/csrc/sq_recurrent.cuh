@@ -124,11 +124,11 @@ struct RGeo {
   static constexpr size_t FIXED = ((size_t)RING * sizeof(RowVectors<D, float>) + 2 * RED * 4 + 127) / 128 * 128;
   static constexpr size_t STATE = (size_t)D * D * 4;
   // fp32 pools: the next tile's state. Packed pools: the fp32 state on its way
-  // between the record's thread map and this kernel's, the next tile's
-  // record, the record going out with the head's row tables
+  // between the record's thread map and this kernel's (and then the record
+  // going out), the next tile's record, the head's row tables; at 8 bits and
+  // D = 128 two CTAs fit per SM
   static size_t smem(bool packed, uint32_t rec) {
-    const size_t r = (rec + 127) / 128 * 128;
-    return FIXED + STATE + (packed ? 2 * r + 7 * D : 0);
+    return FIXED + STATE + (packed ? (rec + 127) / 128 * 128 + 7 * D : 0);
   }
 };
 
@@ -178,13 +178,10 @@ __device__ __forceinline__ void unpack_record(const RecordMap<D>& m, const uint8
   }
 }
 
-// The head's tables that the quantization reads: D row impacts, row offsets,
-// row widths (7 D bytes behind the record), on their way to shared memory.
+// The head's tables that the quantization reads (D row impacts, row offsets,
+// row widths: 7 D bytes), on their way to shared memory.
 template <int D>
-__device__ __forceinline__ uint8_t* pack_tables(uint8_t* rec, uint32_t rb) { return rec + (rb + 15) / 16 * 16; }
-template <int D>
-__device__ __forceinline__ void fetch_pack_tables(const RaggedArgs& a, int h, uint8_t* rec) {
-  uint8_t* t = pack_tables<D>(rec, a.t.rec_bytes[h]);
+__device__ __forceinline__ void fetch_pack_tables(const RaggedArgs& a, int h, uint8_t* t) {
   for (int x = threadIdx.x; x < 7 * D / 4; x += Geo<D>::NT) {
     const uint8_t* src = x < D ? reinterpret_cast<const uint8_t*>(a.t.phi + (size_t)h * D + x)
                          : x < D + D / 2 ? reinterpret_cast<const uint8_t*>(a.t.row_off + (size_t)h * D) + 4 * (x - D)
@@ -194,24 +191,24 @@ __device__ __forceinline__ void fetch_pack_tables(const RaggedArgs& a, int h, ui
   sqk::cp_async_commit();
 }
 // S [D][D] in shared memory, quantized into the slot's record (the
-// quantization of sq_quantize_state), with the tables of fetch_pack_tables
-// behind `rec`. `sync`: a barrier of the Geo<D>::NT threads that call it;
-// one has passed since S and the tables were complete. Returns status bits.
+// quantization of sq_quantize_state) with the tables of fetch_pack_tables.
+// The record is built where S was. `sync`: a barrier of the Geo<D>::NT
+// threads that call it; one has passed since S and the tables were complete.
+// Returns status bits.
 template <int D, typename Sync>
-__device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8_t* dst, uint8_t* rec, const float* S,
+__device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8_t* dst, float* S, const uint8_t* tables,
                                                Sync sync) {
   using G = Geo<D>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cc = lane % G::LPR, rg = warp * G::RPW + lane / G::LPR;
   const uint32_t rb = a.t.rec_bytes[h];
-  const float* phi = reinterpret_cast<const float*>(pack_tables<D>(rec, rb));
+  uint8_t* rec = reinterpret_cast<uint8_t*>(S);
+  const float* phi = reinterpret_cast<const float*>(tables);
   const uint16_t* row_off = reinterpret_cast<const uint16_t*>(phi + D);
   const uint8_t* row_code = reinterpret_cast<const uint8_t*>(row_off + D);
   float4 icol[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) icol[p] = *reinterpret_cast<const float4*>(a.t.icol + (size_t)h * D + 16 * cc + 4 * p);
-  if (tid < 1) *reinterpret_cast<uint4*>(rec + rb - 16) = make_uint4(0, 0, 0, 0);  // the padding's bytes
-  sync();
   float2 T[G::RPT][8];
 #pragma unroll
   for (int r = 0; r < G::RPT; ++r)
@@ -221,6 +218,9 @@ __device__ __forceinline__ uint32_t pack_state(const RaggedArgs& a, int h, uint8
       T[r][2 * p] = __fmul2_rn(make_float2(x.x, x.y), make_float2(icol[p].x, icol[p].y));
       T[r][2 * p + 1] = __fmul2_rn(make_float2(x.z, x.w), make_float2(icol[p].z, icol[p].w));
     }
+  sync();  // S has been read
+  if (tid == 0) *reinterpret_cast<uint4*>(rec + rb - 16) = make_uint4(0, 0, 0, 0);  // the padding's bytes
+  sync();
   const uint32_t st = sqk::requant_rows<D, 0>(rec, row_off, row_code, phi, rg, cc, false, T);
   sync();
   for (uint32_t x = tid * 16; x < rb; x += G::NT * 16)
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   float* red = reinterpret_cast<float*>(smem + R::RING * sizeof(RowVectors<D, float>));  // two rows' partials
   float* Ssh = reinterpret_cast<float*>(smem + R::FIXED);  // fp32 pools: the incoming state; packed: see RGeo
   uint8_t* rec_in = smem + R::FIXED + R::STATE;
+  uint8_t* tables = rec_in + (a.rec_cap + 127) / 128 * 128;
   __shared__ RowTile tiles[3];                   // this one, the next, the one behind it
   __shared__ TileSearch search;
   __shared__ __align__(8) uint64_t arrived;      // the incoming state or record
@@ -363,14 +364,13 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   float4 S[R::RPT];
   bool ok = true;
   if (PACKED) {
-    uint8_t* rec_out = rec_in + (a.rec_cap + 127) / 128 * 128;
     if (resume) {
       RecordMap<D> m;
       map_record<D>(a, c.h, m);
       ok = sqk::mbar_wait_bounded(&arrived, phase & 1, a.wait_ns);
       if (ok) unpack_record<D>(m, rec_in, Ssh);
     }
-    if (c.what & TILE_RUN) fetch_pack_tables<D>(a, c.h, rec_out);
+    if (c.what & TILE_RUN) fetch_pack_tables<D>(a, c.h, tables);
     __syncthreads();
   } else if (resume) {
     ok = sqk::mbar_wait_bounded(&arrived, phase & 1, a.wait_ns);
@@ -487,10 +487,9 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
     if (PACKED) {
 #pragma unroll
       for (int r = 0; r < R::RPT; ++r) *reinterpret_cast<float4*>(Ssh + (row0 + r) * D + c4) = S[r];
-      uint8_t* rec_out = rec_in + (a.rec_cap + 127) / 128 * 128;
       cp_async_wait_all_groups();  // the tables (and the next rows)
       __syncthreads();
-      st |= pack_state<D>(a, c.h, record_of(c), rec_out, Ssh, [] { __syncthreads(); });
+      st |= pack_state<D>(a, c.h, record_of(c), Ssh, tables, [] { __syncthreads(); });
     } else {
       float* S_pool = state_of(c);
 #pragma unroll
