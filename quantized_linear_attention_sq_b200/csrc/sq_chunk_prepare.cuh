@@ -15,11 +15,11 @@
 // precision behind a gate of zero. Decays are products of factors that are
 // all at most one (token to the end of its 16, from the start of its 16,
 // between 16s; inside a 16 the quotient of two of them), so a block needs a
-// few hundred exponentials, not one for each pair. The inverse goes by blocks of 16: those on the diagonal
-// by substitution in fp32, then pairs of blocks, [T1 0; -T2 A21 T1, T2], to
-// 32 and to 64 on the tensor cores, every operand as three bf16 terms whose
-// sum is the fp32 value (the six largest of nine products: fp32 accuracy).
-// T leaves as those terms; P T only reaches o, a bf16 result, and is formed
+// few hundred exponentials, not one for each pair. The inverse goes by blocks
+// of 16: those on the diagonal by substitution in fp32, then pairs of blocks,
+// [T1 0; -T2 A21 T1, T2], to 32 and to 64 on the tensor cores, every operand
+// as three bf16 terms whose sum is the fp32 value (the six largest of nine
+// products: fp32 accuracy). T leaves as those terms; P T only reaches o, a bf16 result, and is formed
 // from and stored as two (2^-16). Only the blocks on and below the diagonal
 // are stored, in the order the scan's matrix instructions read them.
 // Bound by latency: a value head is a chain of six short phases with a
@@ -61,12 +61,11 @@ struct PrepArgs {
 
 // The block's request, first row and rows; false where there is nothing to do.
 __device__ __forceinline__ bool block_span(const PrepArgs& a, int c, int& first, int& n) {
-  if (c >= a.cu_blocks[a.r.B]) return false;
-  const int b = a.block_req[c];
-  if (b < 0 || b >= a.r.B) return false;
+  const int blocks = a.cu_blocks[a.r.B], b = a.block_req[c];  // two loads at once, then three
+  if (c >= blocks || b < 0 || b >= a.r.B) return false;
+  const int at = c - a.cu_blocks[b];
   int r0, len;
   ragged_span(a.r, b, r0, len);
-  const int at = c - a.cu_blocks[b];
   if (len < a.r.min_long || at < 0 || at >= (len + 63) / 64) return false;
   first = r0 + 64 * at;
   n = min(64, len - 64 * at);
@@ -212,17 +211,19 @@ __device__ __forceinline__ float pair_diff(float2 a, float2 b) {
   return __fadd_rn(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y));
 }
 
-// Gates, betas and decay factors of value heads h and h + 1 (`heads` of
-// them), a thread for each row of each; `rec`: their records, whose factors
-// are written here.
-__device__ __forceinline__ void prepare_gates(const PrepArgs& a, PrepSmem& sm, uint8_t* rec, int first, int n, int h,
-                                              int heads) {
+// Gates and betas of value heads h and h + 1 (`heads` of them), a thread for
+// each row of each.
+__device__ __forceinline__ float2 load_gates(const PrepArgs& a, int first, int n, int h, int heads) {
+  const int which = threadIdx.x >> 6, i = threadIdx.x & 63;
+  const size_t at = (size_t)(first + min(i, n - 1)) * a.r.h_v + h + (which < heads ? which : 0);
+  return i < n ? make_float2(a.r.g[at], a.r.beta[at]) : make_float2(1.0f, 0.0f);
+}
+// Their decay factors; `rec`: their records, whose factors are written here.
+__device__ __forceinline__ void prepare_gates(PrepSmem& sm, uint8_t* rec, float2 gb, int heads) {
   const int tid = threadIdx.x, lane = tid & 31, which = tid >> 6, i = tid & 63;
   const bool on = which < heads;
   PrepGate& s = sm.gate[which];
-  const size_t at = (size_t)(first + min(i, n - 1)) * a.r.h_v + h + (on ? which : 0);
-  const float g = i < n ? clamp_gate(a.r.g[at]) : 1.0f;
-  const float beta = i < n ? a.r.beta[at] : 0.0f;
+  const float g = clamp_gate(gb.x), beta = gb.y;
   // a gate of zero counts as 2^-126; a NaN stays one. log2f is good to an
   // ulp: over decays that matter the sum of those errors is below 2^-22.
   float2 G = make_float2(log2f(g < 1.17549435e-38f ? 1.17549435e-38f : g), 0.0f);
@@ -265,6 +266,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
   int first, n;
   if (!block_span(a, c, first, n)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int share = a.r.h_v / a.r.h_k;
+  float2 gb = load_gates(a, first, n, hk * share, min(2, share));  // with the tiles
 #pragma unroll 8
   for (int x = tid; x < 2 * 64 * 16; x += kPrepThreads) {
     const int which = x >> 10, row = (x >> 4) & 63, piece = x & 15;
@@ -296,7 +299,6 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
       dot[x].add(fa, fb);
     }
   }
-  const int share = a.r.h_v / a.r.h_k;
   const int j2 = 2 * (lane & 3), r4 = lane >> 2;
   const int piece = blk_piece(lane & 15, lane >> 4);  // this lane's row of a matrix load
   const int left = blk_piece(r4, 0) + 2 * j2, turn = blk_piece(0, 1) - 2 * (blk_piece(r4, 0) & 16);  // see put_left
@@ -304,7 +306,10 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
   for (int hh = 0; hh < share; ++hh) {
     const int h = hk * share + hh;
     uint8_t* rec = a.ws + ((uint64_t)c * a.r.h_v + h) * kPrepBytes;
-    if ((hh & 1) == 0) prepare_gates(a, s, rec, first, n, h, min(2, share - hh));
+    if ((hh & 1) == 0) {
+      prepare_gates(s, rec, gb, min(2, share - hh));
+      if (hh + 2 < share) gb = load_gates(a, first, n, h + 2, min(2, share - hh - 2));
+    }
     const PrepGate& gt = s.gate[hh & 1];
     __syncthreads();  // the factors; the tiles (first head) or the previous head's matrices have been read
 #pragma unroll
