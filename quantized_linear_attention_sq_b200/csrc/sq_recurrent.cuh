@@ -85,6 +85,17 @@ __device__ __forceinline__ void store4(__half* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// x *= f, y += x f, two elements an instruction.
+__device__ __forceinline__ void mul4(float4& x, float f) {
+  const float2 a = __fmul2_rn(make_float2(x.x, x.y), make_float2(f, f));
+  const float2 b = __fmul2_rn(make_float2(x.z, x.w), make_float2(f, f));
+  x = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void fma4(float4& y, const float4& x, float f) {
+  const float2 a = __ffma2_rn(make_float2(x.x, x.y), make_float2(f, f), make_float2(y.x, y.y));
+  const float2 b = __ffma2_rn(make_float2(x.z, x.w), make_float2(f, f), make_float2(y.z, y.w));
+  y = make_float4(a.x, a.y, b.x, b.y);
+}
 // Four elements as fp32.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -411,9 +422,8 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         float4& x = S[r4 + y];
-        x.x *= gg[y]; x.y *= gg[y]; x.z *= gg[y]; x.w *= gg[y];
-        p.x = fmaf(x.x, kk[y], p.x); p.y = fmaf(x.y, kk[y], p.y);
-        p.z = fmaf(x.z, kk[y], p.z); p.w = fmaf(x.w, kk[y], p.w);
+        mul4(x, gg[y]);
+        fma4(p, x, kk[y]);
       }
     }
     auto deposit = [&](float4 x, float* to) {
@@ -432,9 +442,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
       const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const float4& x = S[r4 + y];
-        p.x = fmaf(x.x, qq[y], p.x); p.y = fmaf(x.y, qq[y], p.y);
-        p.z = fmaf(x.z, qq[y], p.z); p.w = fmaf(x.w, qq[y], p.w);
+        fma4(p, S[r4 + y], qq[y]);
       }
     }
     deposit(p, rd + (R::NW + warp) * D);
@@ -469,9 +477,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
       const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        float4& x = S[r4 + y];
-        x.x = fmaf(kk[y], u.x, x.x); x.y = fmaf(kk[y], u.y, x.y);
-        x.z = fmaf(kk[y], u.z, x.z); x.w = fmaf(kk[y], u.w, x.w);
+        fma4(S[r4 + y], u, kk[y]);
       }
     }
   }
