@@ -4,7 +4,7 @@
 //
 // One CTA per (request, value head), one per SM. The transposed state S^T
 // [128 value columns][128 key rows] lives in registers in fp32 (a thread owns
-// one value column and half of the key rows) and all four products of a block
+// one value column and a quarter of the key rows) and all four products of a block
 // run on the tensor cores with a transposed left operand out of tensor
 // memory, so no operand that a thread computes ever goes through shared
 // memory:
@@ -24,7 +24,15 @@
 // issues the matrix products. The chain of a block is D1k -> r -> D2 -> u ->
 // D3 -> S; D3 and S go by halves of the key rows, so that the second half of
 // D3 and the first of the next D1k run under S. The q product runs under r, o
-// is finished under D3 and leaves under the next D1k.
+// is finished and leaves under D3, and the next block's rows are taken in under
+// the next D1k; v and o pass between rows and tensor memory by ldmatrix and
+// stmatrix.
+// Bound by the latency of that chain: about 5.25 k cycles a block (32 requests
+// of 2048 rows with 32 heads: 710 us; one request of 32768 rows: 1422 us); in
+// 24 requests of 0..1900 rows the tensor pipe is active 40 % of the time and a
+// scheduler issues 0.48 instructions a cycle. With two terms for S the 32
+// requests took 756 us where three took 822, but the state's error against 64
+// bits rose from 2.4e-7 to 1.0e-6: three stay.
 #pragma once
 
 #include <cuda.h>

@@ -5,7 +5,10 @@
 // 16-bit type, two of fp32), so d / 8 lanes hold a head: the sum of squares
 // is log2(d / 8) shuffles, and the rotation's partner channels are in the
 // same thread (adjacent pairs) or a fixed number of lanes away (halves).
-// Bound by HBM: every element is read once and written once. The angles of a
+// Every element is read once and written once: 16384 rows x 32 heads of 128
+// bf16, half rotated, take 71 us, 0.58 of the measured copy rate. Bound by
+// issue and latency: 186 warp instructions per 256 elements, 0.69 issued a
+// cycle and scheduler, most stalls on shuffles and shared memory. The angles of a
 // row are shared by all its heads: a CTA takes groups of `rows_per_cta` rows
 // and forms their rot_dim / 2 sines and cosines once into shared memory, a
 // group ahead (position times frequency in turns, in fp64, reduced to half a
