@@ -138,11 +138,11 @@ typedef struct {
  *            used by this call's kernels only while they run: calls that may
  *            overlap (two streams, two graphs in flight) need one each
  * SQ_BF16 requests of SQ_GATE_HEAD pools with d = 128 that are not very short
- * run in blocks of 64 rows on the tensor cores: the state stays accurate to
- * fp32 (operands are split into bf16 terms), so it differs from a row by row
- * run in its last bits only. All others run row by row in fp32. A NaN or an
- * infinity in a row reaches the state and o from its block of 64 rows on, and
- * no other request. */
+ * run in blocks of 64 rows on the tensor cores: the state, and o before it is
+ * rounded, stay accurate to fp32 (operands are split into three bf16 terms),
+ * so they differ from a row by row run in their last bits only. All others
+ * run row by row in fp32. A NaN or an infinity in a row reaches the state and
+ * o from its block of 64 rows on, and no other request. */
 sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void* k, const void* v, int64_t q_row_stride,
                             int64_t k_row_stride, int64_t v_row_stride, int32_t dtype, const float* beta,
                             const float* g, void* o, const sq_ragged_tables* tables, const int32_t* slot_ids, int32_t B,

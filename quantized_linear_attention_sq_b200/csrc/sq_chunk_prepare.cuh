@@ -19,8 +19,9 @@
 // of 16: those on the diagonal by substitution in fp32, then pairs of blocks,
 // [T1 0; -T2 A21 T1, T2], to 32 and to 64 on the tensor cores, every operand
 // as three bf16 terms whose sum is the fp32 value (the six largest of nine
-// products: fp32 accuracy). T leaves as those terms; P T only reaches o, a bf16 result, and is formed
-// from and stored as two (2^-16). Only the blocks on and below the diagonal
+// products: fp32 accuracy). T and P T leave as such terms: o may be a small
+// difference of large sums (an old value overwritten by a smaller one), so what
+// reaches it is held like the state's. Only the blocks on and below the diagonal
 // are stored, in the order the scan's matrix instructions read them.
 // Bound by latency: a value head is a chain of six short phases with a
 // barrier between them, and five CTAs per SM run theirs against each other: 485
@@ -35,21 +36,19 @@
 
 namespace sqr {
 
-constexpr int kTerms = 3;                                    // bf16 terms of an fp32 operand of the state's path
-constexpr int kOutTerms = 2;                                 // terms of P T
+constexpr int kTerms = 3;                                    // bf16 terms of an fp32 operand
 constexpr int kTriBytes = 32 * (64 + 48 + 32 + 16);          // one term of one matrix
-constexpr int kTermsBytes = (kTerms + kOutTerms) * kTriBytes;
+constexpr int kTermsBytes = kTerms * 2 * kTriBytes;
 constexpr int kCoefFloats = 4 * 64 + 4;                      // e^G, beta, beta e^G, e^(G_63 - G), e^(G_63)
 constexpr int kPrepBytes = kTermsBytes + 4 * kCoefFloats;    // per block and value head
 static_assert(kPrepBytes % 16 == 0, "bulk copies move 16-byte multiples");
 
-// Terms 0 and 1 hold T and P T: for each 16 columns kk = j / 16, the operand
+// A term holds T and P T: for each 16 columns kk = j / 16, the operand
 // rows that are not all zero there, rows 16 kk .. 63 of T, then the same rows
-// of P T. Term 2 is T alone. Rows come in groups of 8 x 16 columns, a group as
-// two 8 x 8 pieces of 128 contiguous bytes (the tensor core's unswizzled layout).
+// of P T. Rows come in groups of 8 x 16 columns, a group as two 8 x 8 pieces
+// of 128 contiguous bytes (the tensor core's unswizzled layout).
 __host__ __device__ constexpr int term_base(int s) { return s * 2 * kTriBytes; }
-__host__ __device__ constexpr int pair_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }  // within terms 0, 1
-__host__ __device__ constexpr int tri_base(int kk) { return pair_base(kk) / 2; }                 // within term 2
+__host__ __device__ constexpr int pair_base(int kk) { return kk * 4096 - kk * (kk - 1) * 512; }  // within a term
 __device__ __forceinline__ int row_piece(int li, int j) {
   return (li >> 3) * 256 + ((j >> 3) & 1) * 128 + (li & 7) * 16 + (j & 7) * 2;
 }
@@ -97,10 +96,6 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[kTerms]) 
   t[1] = take_bf16x2(a, b);
   t[2] = bf16x2(a, b);
 }
-__device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[kOutTerms]) {
-  t[0] = take_bf16x2(a, b);
-  t[1] = bf16x2(a, b);
-}
 
 constexpr int kPrepThreads = 128;
 constexpr int kTile = 136;   // bf16 per row of the q and k tiles (16 bytes of padding)
@@ -120,16 +115,20 @@ struct PrepGate {
   float hop[4][4];   // e^(R_(bi-1) - R_bj), bj < bi
   int32_t steep[4];  // the 16's decay is below 2^-100: its inverses may overflow, its pairs are formed one by one
 };
+constexpr int kAd = 20;      // floats per row of a block of A on the diagonal
+static_assert(16 * kAd * 4 <= kTerms * kBlk, "one fits where a block of T will be");
 struct PrepSmem {
   union {
     __nv_bfloat16 qk[2][64 * kTile];
     struct {
       uint8_t A[6][kTerms][kBlk];       // blocks below the diagonal
-      uint8_t P[10][kOutTerms][kBlk];   // blocks on and below it
+      uint8_t P[10][kTerms][kBlk];      // blocks on and below it
       uint8_t T[10][kTerms][kBlk];
-      float Ad[4][16][20];              // A's blocks on it
     } m;
   };
+  // A's blocks on the diagonal, 16 rows of kAd floats each: where the last row
+  // of T's blocks (number 3: the one at (2, 0)) is written once they have been read
+  __device__ __forceinline__ float* Ad(int b) { return reinterpret_cast<float*>(m.T[b < 3 ? 6 + b : 3][0]); }
   PrepGate gate[2];  // two value heads at a time
   float2 part[4];    // log gates summed by each warp
 };
@@ -349,34 +348,20 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<float2*>(&s.m.Ad[bi][r4 + 8 * y][j2 + 8 * z]) =
+              *reinterpret_cast<float2*>(s.Ad(bi) + (r4 + 8 * y) * kAd + j2 + 8 * z) =
                   make_float2(m.c[z][2 * y], m.c[z][2 * y + 1]);
           continue;
         }
       }
-      if (which) {
-        Terms t;
-        acc_terms(m, t);
-        uint8_t* dst = s.m.A[below(bi, bj)][0] + left;
+      Terms t;
+      acc_terms(m, t);
+      uint8_t* dst = (which ? s.m.A[below(bi, bj)][0] : s.m.P[tri(bi, bj)][0]) + left;
 #pragma unroll
-        for (int u = 0; u < kTerms; ++u) put_left(dst + u * kBlk, turn, t[u]);
-      } else {
-        uint8_t* dst = s.m.P[tri(bi, bj)][0] + left;
-        uint32_t t0[4], t1[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          uint32_t w[kOutTerms];
-          split2(m.c[z >> 1][2 * (z & 1)], m.c[z >> 1][2 * (z & 1) + 1], w);
-          t0[z] = w[0];
-          t1[z] = w[1];
-        }
-        put_left(dst, turn, t0);
-        put_left(dst + kBlk, turn, t1);
-      }
+      for (int u = 0; u < kTerms; ++u) put_left(dst + u * kBlk, turn, t[u]);
     }
     __syncthreads();
     {  // the block on the diagonal: lane owns a column of its warp's (both half warps the same)
-      const float (*Ad)[20] = s.m.Ad[warp];
+      const float* Ad = s.Ad(warp);
       const int col = lane & 15, half = lane >> 4;
       float t[16];
 #pragma unroll
@@ -384,7 +369,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
         float acc = i == col ? 1.0f : 0.0f;
 #pragma unroll
         for (int l = 0; l < i; l += 4) {  // A is 0 on its diagonal block's diagonal and above
-          const float4 c = *reinterpret_cast<const float4*>(&Ad[i][l]);
+          const float4 c = *reinterpret_cast<const float4*>(Ad + i * kAd + l);
           acc = fmaf(-c.x, t[l], acc);
           if (l + 1 < i) acc = fmaf(-c.y, t[l + 1], acc);
           if (l + 2 < i) acc = fmaf(-c.z, t[l + 2], acc);
@@ -453,31 +438,29 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_chunk_prepare(const PrepArg
       acc.zero();
 #pragma unroll 1
       for (int l = pj; l <= pi; ++l) {
-        uint32_t pa[kOutTerms][4], tb[kOutTerms][4];
+        Terms pa, tb;
 #pragma unroll
-        for (int u = 0; u < kOutTerms; ++u) {
+        for (int u = 0; u < kTerms; ++u) {
           ldmatrix4(pa[u], s.m.P[tri(pi, l)][u] + piece);
           ldmatrix4t(tb[u], s.m.T[tri(l, pj)][u] + piece);
         }
-        acc.add(pa[1], tb[0]);
-        acc.add(pa[0], tb[1]);
-        acc.add(pa[0], tb[0]);
+        add6(acc, pa, tb);
       }
       // T: the warp's 32 pieces of a term are 512 contiguous bytes of the record
       uint8_t* out = rec + row_piece(lane & 15, 8 * (lane >> 4)) + 512 * (pi - pj);
 #pragma unroll
       for (int u = 0; u < kTerms; ++u)
-        *reinterpret_cast<uint4*>(out + term_base(u) + (u == 2 ? tri_base(pj) : pair_base(pj))) =
+        *reinterpret_cast<uint4*>(out + term_base(u) + pair_base(pj)) =
             *reinterpret_cast<const uint4*>(s.m.T[tri(pi, pj)][u] + piece);
       // P T: rows 64 - 16 pj of the operand on, row 16 (pi - pj) + ... of them
       uint8_t* o_at = rec + pair_base(pj) + 512 * (4 + pi - 2 * pj) + row_piece(r4, j2);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
-        uint32_t t[kOutTerms];
-        split2(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1], t);
+        uint32_t t[kTerms];
+        split3(acc.c[z >> 1][2 * (z & 1)], acc.c[z >> 1][2 * (z & 1) + 1], t);
         uint8_t* o2 = o_at + row_piece(8 * (z & 1), 8 * (z >> 1));
-        *reinterpret_cast<uint32_t*>(o2 + term_base(0)) = t[0];
-        *reinterpret_cast<uint32_t*>(o2 + term_base(1)) = t[1];
+#pragma unroll
+        for (int u = 0; u < kTerms; ++u) *reinterpret_cast<uint32_t*>(o2 + term_base(u)) = t[u];
       }
     }
   }

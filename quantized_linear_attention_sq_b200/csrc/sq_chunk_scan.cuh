@@ -13,10 +13,9 @@
 //     D3 = (e^(G63 - G) u)^T k  (A: u^T,  B: the k tile again, read the other way)
 // with r = beta (v - e^G D1k), u = D2u, o = e^G D1q + D2o, S <- e^(G63) S + D3 in
 // fp32 by the threads. S, r and u are split into three bf16 terms (T and P T
-// are stored so), k and q are bf16 already: D1k and D3 take three products,
-// D2 the six largest of nine, so that the state is fp32-accurate; what only
-// reaches o, which is bf16, takes two terms (D1q) and three products (the P T
-// half of D2): 2^-16. The state adds one fresh accumulator per block in fp32:
+// are stored so), k and q are bf16 already: D1 and D3 take three products,
+// D2 the six largest of nine, so that the state, and o before its rounding to
+// bf16, are fp32-accurate. The state adds one fresh accumulator per block in fp32:
 // the tensor core never accumulates across blocks.
 //
 // Eighteen warps: sixteen compute (four per 32 lanes of tensor memory, sharing
@@ -423,15 +422,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (elect_one()) {
         tc_commit(&ctl.d1);
 #pragma unroll
-        for (int s = 1; s >= 0; --s)
+        for (int s = kTerms - 1; s >= 0; --s)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             tc_mma(tm + TM_D1Q, tm + TM_S + s_col(s, ks), qt + ((ks >> 2) * kTileBytes + (ks & 3) * 32) / 16,
-                   mma_desc(64, false, s), s < 1 || ks > 0);
+                   mma_desc(64, false, s), s < kTerms - 1 || ks > 0);
       }
       __syncwarp();
       // rows 16 kk .. 63 of T see columns 16 kk .. 16 kk + 15: the six largest products of terms of r and of T, the
-      // largest last; then the three largest for P T
+      // largest last; then the same for P T
       if (!warp_wait(ctl, &ctl.r_ready, ph, ns)) break;
       tc_after();
       if (elect_one()) {
@@ -442,16 +441,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tm + TM_D2 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
-                   prep + (term_base(pt[x]) + (pt[x] == 2 ? tri_base(kk) : pair_base(kk))) / 16,
+                   prep + (term_base(pt[x]) + pair_base(kk)) / 16,
                    mma_desc(64 - 16 * kk, false, pr[x]), x > 0 || kk > 0);
         tc_commit(&ctl.d2);
 #pragma unroll
-        for (int x = 3; x < 6; ++x)
+        for (int x = 0; x < 6; ++x)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // P T follows T's 64 - 16 kk rows, 32 bytes each
             tc_mma(tm + TM_D2 + 64 + 16 * kk, tm + TM_R + 32 * pr[x] + 8 * kk,
                    prep + (term_base(pt[x]) + pair_base(kk) + 32 * (64 - 16 * kk)) / 16,
-                   mma_desc(64 - 16 * kk, false, pr[x]), x > 3 || kk > 0);
+                   mma_desc(64 - 16 * kk, false, pr[x]), x > 0 || kk > 0);
         tc_commit(&ctl.d2o);
       }
       __syncwarp();
