@@ -54,12 +54,14 @@ constexpr uint32_t kStageBytes = kStagePrep + (kPrepBytes + 1023) / 1024 * 1024;
 constexpr uint32_t kStageTx = kStagePrep + kPrepBytes;
 constexpr uint32_t kOutAt = kScanStages * kStageBytes;  // o rows on their way out
 
+constexpr int kRanked = 256;  // most requests that are taken by length, see request_of
 struct ScanCtl {
   uint64_t full[kScanStages], empty[kScanStages];
   uint64_t s_ready[2], d3[2];
   uint64_t r_ready, u_ready, d1, d2, d2o, o_ready, o_free, drain;
   uint32_t tmem;
   int32_t abort, request;
+  alignas(16) int32_t length[kRanked];  // of request_of: not where TMA writes, which ordinary stores are not ordered with
 };
 constexpr size_t kScanSmem = 1024 + kOutAt + kTileBytes + sizeof(ScanCtl) + 16;
 
@@ -234,8 +236,7 @@ __device__ __forceinline__ void record_sync() { asm volatile("bar.sync 1, 256;" 
 // longest start first, so that no long one is left to run alone (24 requests
 // of 0..1900 rows: 146 us in their own order, 113 by length); with more
 // the order matters little and the search would take long.
-constexpr int kRanked = 256;
-__device__ __forceinline__ int request_of(const RaggedArgs& a, int rank, int32_t* length, int32_t* found) {
+__device__ __forceinline__ int request_of(const RaggedArgs& a, int rank, ScanCtl& ctl) {
   if (a.B > kRanked || a.B == 1) return rank;
   const int tid = threadIdx.x, padded = (a.B + 3) & ~3;
   int n = -1;
@@ -243,19 +244,19 @@ __device__ __forceinline__ int request_of(const RaggedArgs& a, int rank, int32_t
     int first;
     ragged_span(a, tid, first, n);
   }
-  if (tid < padded) length[tid] = n;
+  if (tid < padded) ctl.length[tid] = n;
   __syncthreads();
   if (tid < a.B) {
     int before = 0;
     for (int j = 0; j < padded; j += 4) {
-      const int4 l = *reinterpret_cast<const int4*>(length + j);
+      const int4 l = *reinterpret_cast<const int4*>(ctl.length + j);
       before += (l.x > n || (l.x == n && j < tid)) + (l.y > n || (l.y == n && j + 1 < tid)) +
                 (l.z > n || (l.z == n && j + 2 < tid)) + (l.w > n || (l.w == n && j + 3 < tid));
     }
-    if (before == rank) *found = tid;
+    if (before == rank) ctl.request = tid;
   }
   __syncthreads();
-  return *found;
+  return ctl.request;
 }
 
 template <bool PACKED>
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const RaggedArgs& a = args.p.r;
   const int rank = blockIdx.x / a.h_v, h = blockIdx.x - rank * a.h_v, hk = h / (a.h_v / a.h_k);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = request_of(a, rank, reinterpret_cast<int32_t*>(smem), &ctl.request);
+  const int b = request_of(a, rank, ctl);
   // everything about the request at once: its loads wait on none of each other
   const int slot = a.slots ? a.slots[b] : b, c0 = args.p.cu_blocks[b];
   const bool resume = a.past && a.past[b] > 0;
