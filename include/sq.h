@@ -288,10 +288,12 @@ sq_status sq_get_exact_count(sq_handle* h, void* stream, uint32_t* count, int32_
 /* Plumbing (no passage). Limit, in nanoseconds, of every bounded wait inside
  * this handle's step kernels (default 2 s; at least 1000). A wait that runs
  * out abandons its tile before anything of it is written and sets
- * SQ_STATUS_TIMEOUT. */
+ * SQ_STATUS_TIMEOUT. The limit holds for sq_prefill_ragged too; what is left
+ * there when one runs out stands in sq_ragged.h. */
 sq_status sq_set_wait_limit(sq_handle* h, uint64_t ns);
 
-/* Testing only (no passage). From the next packed decode step on, the
+/* Testing only (no passage). From the next packed decode step (or
+ * sq_prefill_ragged, see there what a wait that runs out leaves) on, the
  * shared-memory stage that receives tile (request 0, head 0) expects
  * `extra_bytes` (at most 65536) more bytes than are loaded into it, so the
  * wait of the CTA that took that tile runs out after the wait limit: the

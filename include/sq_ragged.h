@@ -142,7 +142,12 @@ typedef struct {
  * rounded, stay accurate to fp32 (operands are split into three bf16 terms),
  * so they differ from a row by row run in their last bits only. All others
  * run row by row in fp32. A NaN or an infinity in a row reaches the state and
- * o from its block of 64 rows on, and no other request. */
+ * o from its block of 64 rows on, and no other request.
+ * A wait that runs out (sq_set_wait_limit) sets SQ_STATUS_TIMEOUT: the CTA
+ * leaves once its copies under way have landed. The state of the (request,
+ * value head) it was at keeps its slot's bytes; row by row its o is untouched
+ * and the further (request, value head)s of that CTA are left out the same
+ * way, in blocks o of blocks before the wait is already written. */
 sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void* k, const void* v, int64_t q_row_stride,
                             int64_t k_row_stride, int64_t v_row_stride, int32_t dtype, const float* beta,
                             const float* g, void* o, const sq_ragged_tables* tables, const int32_t* slot_ids, int32_t B,

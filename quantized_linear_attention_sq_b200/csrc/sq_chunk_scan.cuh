@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       uint8_t* stage = smem + sg * kStageBytes;
       const int row = first + 64 * i;
       if (lane == 0) {
-        sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx);
+        sqk::mbar_arrive_expect_tx(&ctl.full[sg], kStageTx + (b == 0 && h == 0 && i == 0 ? a.test_extra_tx : 0u));
         tma_tile(stage + kTileBytes / 2, &k_map, 0, hk, row, &ctl.full[sg]);
         tma_tile(stage + 3 * kTileBytes / 2, &k_map, 64, hk, row, &ctl.full[sg]);
         tma_tile(stage, &q_map, 0, hk, row, &ctl.full[sg]);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     }
     // no copy is in flight when the CTA ends
     for (int i = max(0, issued - kScanStages); i < issued; ++i)
-      sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, ns);
+      sqk::mbar_wait_bounded(&ctl.full[i & 1], (i >> 1) & 1, a.drain_ns);
     if (lane == 0) sqk::bulk_wait_all();
   } else if (warp == kProductWarp) {  // ------------------------------------- products
     const uint32_t base = sqk::smem_u32(smem);
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // no product is in flight when the tensor memory is given back
     if (elect_one()) tc_commit(&ctl.drain);
     __syncwarp();
-    warp_wait(ctl, &ctl.drain, 0, ns);
+    warp_wait(ctl, &ctl.drain, 0, a.drain_ns);
   } else {  // -------------------------------------------------- the rest
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     auto split_state = [&](int y, uint32_t (&t)[kTerms][8]) {

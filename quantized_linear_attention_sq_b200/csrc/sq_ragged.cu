@@ -379,6 +379,8 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   a.rec_cap = a.fmt_fp32 ? 0u : (uint32_t)h->max_rec;
   a.slot_bytes = h->slot_bytes;
   a.wait_ns = h->wait_ns;
+  a.drain_ns = h->wait_ns > sqi::kWaitNs ? h->wait_ns : sqi::kWaitNs;  // a short limit is no limit for these
+  a.test_extra_tx = h->test_extra_tx;
   a.t = h->tables;
   cudaStream_t st = as_stream(stream);
   const bool blocks = rows > 0 && in_blocks(h, dtype, max_len);

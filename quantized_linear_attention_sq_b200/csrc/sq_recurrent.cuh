@@ -48,6 +48,8 @@ struct RaggedArgs {
   int32_t min_long;           // requests of at least this many rows are another kernel's (0: none is)
   uint32_t rec_cap;           // largest packed record
   uint64_t slot_bytes, wait_ns;
+  uint64_t drain_ns;          // limit of the waits for copies under way after a wait has run out
+  uint32_t test_extra_tx;     // testing only: extra bytes the first wait of tile (request 0, head 0) expects (0: none)
   Tables t;
 };
 
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
   auto bring = [&](const RowTile& t) {  // by one thread
     if (!(t.what & TILE_RESUME)) return;
     const uint32_t bytes = PACKED ? a.t.rec_bytes[t.h] : (uint32_t)R::STATE;
-    sqk::mbar_arrive_expect_tx(&arrived, bytes);
+    sqk::mbar_arrive_expect_tx(&arrived, bytes + (t.b == 0 && t.h == 0 ? a.test_extra_tx : 0u));
     if (PACKED) sqk::bulk_g2s(rec_in, record_of(t), bytes, &arrived);
     else sqk::bulk_g2s(Ssh, state_of(t), bytes, &arrived);
   };
@@ -394,8 +396,11 @@ __global__ void __launch_bounds__(RGeo<D>::NT, 2) k_ragged_rows(const RaggedArgs
     for (int r = 0; r < R::RPT; ++r)
       S[r] = resume && ok ? *reinterpret_cast<const float4*>(Ssh + (row0 + r) * D + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
     cp_async_wait_but_one();  // the first row
-    if (!__syncthreads_and(ok)) {  // the state never came: the pool stays as it is
+    if (!__syncthreads_and(ok)) {  // the state did not come: the CTA's tiles from this one on stay as they are
       st |= sqk::ST_TIMEOUT;
+      // no copy is under way when the CTA ends
+      if (tid == 0) (void)sqk::mbar_wait_bounded(&arrived, (phase - 1) & 1, a.drain_ns);
+      cp_async_wait_all_groups();
       break;
     }
     if (tid == 0) bring(nx);  // every thread has taken this tile's state

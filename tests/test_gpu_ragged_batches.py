@@ -44,3 +44,63 @@ def test_a_request_is_the_same_alone_and_in_a_batch(B, packed):
         assert not bt.h.get_status() & ~_abi.SQ_STATUS_SATURATED
     finally:
         bt.close()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("lengths", [[1, 2, 5, 1], [200, 20, 3, 64], [1] * 400])
+def test_a_wait_that_runs_out_leaves_whole_states(lengths, packed):
+    """The first wait of (request 0, head 0) expects 16 bytes more than are
+    loaded, under a limit of 2 ms: every copy lands, the wait runs out. That
+    state keeps its bytes and its o is not written; whatever else was left
+    out is whole too, and the next call is right again."""
+    hv, B = 4, len(lengths)
+    bt = Batch(lengths, hv=hv, hk=2, packed=packed, past=[3] * B)
+    try:
+        start = bt.pool.clone()
+        bt.run()
+        assert not bt.h.get_status() & ~_abi.SQ_STATUS_SATURATED
+        o, pool = bt.o.clone(), bt.pool.clone()
+        bt.pool.copy_(start)
+        bt.o.fill_(3.0)
+        bt.h.set_wait_limit(2_000_000)
+        bt.h.test_stall_stages(16)
+        bt.run()
+        assert bt.h.get_status() & _abi.SQ_STATUS_TIMEOUT
+
+        def records(p):
+            if not packed:
+                return p
+            at = [bt.h.head_layout(h) for h in range(hv)]
+            per_slot = p.view(bt.n_slots, -1)
+            return [[per_slot[s, off:off + nb] for off, nb in at] for s in range(bt.n_slots)]
+
+        got, old, new = records(bt.pool), records(start), records(pool)
+        left, first = 0, 0
+        for b, n in enumerate(lengths):
+            s = bt.slots[b]
+            for h in range(hv):
+                rows, want = bt.o[first:first + n, h], o[first:first + n, h]
+                if torch.equal(got[s][h], old[s][h]):
+                    left += 1
+                    assert (rows == 3.0).all()
+                else:
+                    assert torch.equal(got[s][h], new[s][h]) and torch.equal(rows, want)
+            first += n
+        assert torch.equal(got[bt.slots[0]][0], old[bt.slots[0]][0])
+        # the tiles of one CTA: (0, 0) and, row by row, every further one of its walk
+        assert 1 <= left <= 1 + B * hv // 128
+        if B * hv <= 128:
+            assert left == 1
+        free = [s for s in range(bt.n_slots) if s not in bt.slots]
+        for s in free:
+            assert all(torch.equal(x, y) for x, y in zip(got[s], old[s]))
+
+        bt.h.test_stall_stages(0)
+        bt.h.set_wait_limit(2_000_000_000)
+        bt.pool.copy_(start)
+        bt.o.fill_(3.0)
+        bt.run()
+        assert torch.equal(bt.o, o) and torch.equal(bt.pool, pool)
+        assert not bt.h.get_status() & ~_abi.SQ_STATUS_SATURATED
+    finally:
+        bt.close()
