@@ -1,0 +1,36 @@
+"""Index arithmetic of the ragged batches at their largest sizes, compiled for
+the host (no GPU needed: the buffers of such a call would fill one)."""
+import shutil
+import subprocess
+
+import pytest
+
+from quantized_linear_attention_sq_b200.build import CSRC
+
+MAIN = r'''
+#include <cstdio>
+#include <initializer_list>
+#include "sq_spans.cuh"
+int main() {
+  for (int32_t n : {0, 1, 63, (1 << 27) - 1, 1 << 27, 1 << 30}) std::printf("pieces %d %lld\n", n, (long long)sqr::row_pieces(n));
+}
+'''
+
+
+@pytest.fixture(scope="module")
+def lines(tmp_path_factory):
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("needs g++")
+    at = tmp_path_factory.mktemp("spans")
+    (at / "main.cpp").write_text(MAIN)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error", "-I", CSRC,
+                    str(at / "main.cpp"), "-o", str(at / "main")], check=True)
+    out = subprocess.run([str(at / "main")], check=True, capture_output=True, text=True).stdout
+    return [line.split() for line in out.splitlines()]
+
+
+def test_pieces_of_the_longest_request(lines):
+    """A bad slot's o is zeroed whole, whatever its length (2^27 rows are 2^31 pieces)."""
+    got = {int(n): int(p) for kind, n, p in (x for x in lines if x[0] == "pieces")}
+    assert got == {n: 16 * n for n in (0, 1, 63, 2 ** 27 - 1, 2 ** 27, 2 ** 30)}
