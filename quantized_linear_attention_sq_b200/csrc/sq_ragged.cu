@@ -14,6 +14,7 @@
 #include "sq_qknorm.cuh"
 #include "sq_ragged.h"
 #include "sq_recurrent.cuh"
+#include "sq_spans.cuh"
 #include "sq_tables.cuh"
 
 using sqi::cuda_fail;
@@ -182,7 +183,7 @@ sq_status start_blocks(const sq_handle* h, const sqr::RaggedArgs& r, const sq_ra
   b.a.p.cu_blocks = t.cu_blocks;
   b.a.p.block_req = t.block_req;
   b.a.p.ws = static_cast<uint8_t*>(workspace);
-  b.a.p.n_blocks = r.rows / SQ_RAGGED_BLOCK + r.B;
+  b.a.p.n_blocks = (int32_t)sqr::most_blocks(r.rows, r.B);
   sq_status s = row_map(&b.q, "q", r.q, r.q_stride, r.h_k, r.rows);
   if (s == SQ_OK) s = row_map(&b.k, "k", r.k, r.k_stride, r.h_k, r.rows);
   if (s == SQ_OK) s = row_map(&b.v, "v", r.v, r.v_stride, r.h_v, r.rows);
@@ -322,9 +323,11 @@ sq_status sq_ragged_workspace_bytes(const sq_handle* h, int32_t dtype, int32_t B
   if (dtype < SQ_F32 || dtype > SQ_F16) return fail(SQ_ERR_INVALID_ARG, "bad element type %d", dtype);
   if (B < 0 || rows < 0 || max_len < 0)
     return fail(SQ_ERR_INVALID_ARG, "B, rows and max_len must be >= 0 (got %d, %d, %d)", B, rows, max_len);
+  if (B > SQ_RAGGED_MAX_REQUESTS)
+    return fail(SQ_ERR_UNSUPPORTED, "B = %d is above %d requests", B, SQ_RAGGED_MAX_REQUESTS);
   if (rows > kMaxRows) return fail(SQ_ERR_UNSUPPORTED, "rows = %d is above %d", rows, kMaxRows);
   *bytes = in_blocks(h, dtype, max_len)
-               ? (uint64_t)(rows / SQ_RAGGED_BLOCK + B) * (uint64_t)h->desc.h_v * sqr::kPrepBytes : 0;
+               ? (uint64_t)sqr::most_blocks(rows, B) * (uint64_t)h->desc.h_v * sqr::kPrepBytes : 0;
   return SQ_OK;
 }
 
@@ -337,8 +340,6 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   uint64_t need = 0;
   sq_status s = sq_ragged_workspace_bytes(h, dtype, B, rows, max_len, &need);
   if (s != SQ_OK) return s;
-  if (B > SQ_RAGGED_MAX_REQUESTS)
-    return fail(SQ_ERR_UNSUPPORTED, "B = %d is above %d requests", B, SQ_RAGGED_MAX_REQUESTS);
   if ((int64_t)B * h->desc.h_v > (int64_t)INT32_MAX / 2) return fail(SQ_ERR_INVALID_ARG, "B too large");
   if (B == 0) return SQ_OK;
   SQ_NEED(pool, 16);
@@ -386,7 +387,7 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
   const bool blocks = rows > 0 && in_blocks(h, dtype, max_len);
   Blocks bl;
   if (blocks) {
-    if (((int64_t)rows / SQ_RAGGED_BLOCK + B) * h->desc.h_k > (int64_t)INT32_MAX)
+    if (sqr::most_blocks(rows, B) * h->desc.h_k > (int64_t)INT32_MAX)
       return fail(SQ_ERR_UNSUPPORTED, "too many blocks of rows");
     a.min_long = kMinLong;
     s = start_blocks(h, a, *tables, workspace, st, bl);

@@ -104,3 +104,17 @@ def test_a_wait_that_runs_out_leaves_whole_states(lengths, packed):
         assert not bt.h.get_status() & ~_abi.SQ_STATUS_SATURATED
     finally:
         bt.close()
+
+
+def test_workspace_of_too_many_requests_is_refused():
+    from quantized_linear_attention_sq_b200.state import StatePool
+    sp = StatePool(1, 4, 2, 128, _abi.SQ_GATE_HEAD, _abi.SQ_FMT_FP32)
+    try:
+        most = _abi.SQ_RAGGED_MAX_REQUESTS
+        one = sp.ragged_workspace_bytes(1, 10)
+        assert one > 0 and sp.ragged_workspace_bytes(most, 2 ** 30) == (2 ** 24 + most) * one
+        for B in (most + 1, 2 ** 31 - 1):
+            with pytest.raises(_abi.SQError, match="requests"):
+                sp.ragged_workspace_bytes(B, 2 ** 30)
+    finally:
+        sp.close()

@@ -13,6 +13,7 @@ MAIN = r'''
 #include "sq_spans.cuh"
 int main() {
   for (int32_t n : {0, 1, 63, (1 << 27) - 1, 1 << 27, 1 << 30}) std::printf("pieces %d %lld\n", n, (long long)sqr::row_pieces(n));
+  for (int32_t b : {0, 1, 16384, 2147483647}) std::printf("blocks %d %lld\n", b, (long long)sqr::most_blocks(1 << 30, b));
 }
 '''
 
@@ -34,3 +35,8 @@ def test_pieces_of_the_longest_request(lines):
     """A bad slot's o is zeroed whole, whatever its length (2^27 rows are 2^31 pieces)."""
     got = {int(n): int(p) for kind, n, p in (x for x in lines if x[0] == "pieces")}
     assert got == {n: 16 * n for n in (0, 1, 63, 2 ** 27 - 1, 2 ** 27, 2 ** 30)}
+
+
+def test_blocks_of_the_largest_batch(lines):
+    got = {int(b): int(n) for kind, b, n in (x for x in lines if x[0] == "blocks")}
+    assert got == {b: 2 ** 24 + b for b in (0, 1, 16384, 2 ** 31 - 1)}
