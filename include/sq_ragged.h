@@ -129,8 +129,9 @@ typedef struct {
  *   o        device, type `dtype`, contiguous [rows, h_v, d]; rows of no
  *            request are left as they were; must not overlap an input
  *   slot_ids device int32 [B] (distinct), or NULL for slots 0..B-1; a
- *            request whose slot is out of range gets o = 0 and
- *            SQ_STATUS_BAD_SLOT, and no state
+ *            request whose slot is out of range, or whose first block (where
+ *            it runs in blocks) no table of these sizes can hold, gets o = 0
+ *            and SQ_STATUS_BAD_SLOT, and no state
  *   rows     rows of q, k, v, beta, g and o; table entries are cut to it
  *   max_len  the longest request's rows as far as the host knows (rows if it
  *            does not): it chooses the kernels, longer requests stay correct

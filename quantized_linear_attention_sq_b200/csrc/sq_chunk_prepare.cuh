@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 
 #include "sq_recurrent.cuh"
+#include "sq_spans.cuh"
 
 namespace sqr {
 
@@ -65,7 +66,7 @@ struct PrepArgs {
 __device__ __forceinline__ bool block_span(const PrepArgs& a, int c, int& first, int& n) {
   const int blocks = a.cu_blocks[a.r.B], b = a.block_req[c];  // two loads at once, then three
   if (c >= blocks || b < 0 || b >= a.r.B) return false;
-  const int at = c - a.cu_blocks[b];
+  const int at = block_after(c, a.cu_blocks[b]);
   int r0, len;
   ragged_span(a.r, b, r0, len);
   if (len < a.r.min_long || at < 0 || at >= (len + 63) / 64) return false;

@@ -38,7 +38,6 @@
 #include <cuda_bf16.h>
 
 #include "sq_chunk_prepare.cuh"
-#include "sq_spans.cuh"
 
 namespace sqr {
 
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   }
   const int blocks = (n + 63) >> 6;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
-  if (slot < 0 || slot >= a.n_slots || c0 < 0 || c0 + blocks > args.p.n_blocks) {
+  if (slot < 0 || slot >= a.n_slots || !blocks_within(c0, blocks, args.p.n_blocks)) {
     const int64_t pieces = row_pieces(n);
     for (int64_t x = tid; x < pieces; x += kScanThreads)
       reinterpret_cast<uint4*>(out + ((size_t)(first + (x >> 4)) * a.h_v + h) * 128)[x & 15] = make_uint4(0, 0, 0, 0);

@@ -17,4 +17,10 @@ SQ_HD int64_t row_pieces(int32_t n) { return (int64_t)n * 16; }
 // Most blocks of 64 rows that B requests with `rows` rows in all can have.
 SQ_HD int64_t most_blocks(int32_t rows, int32_t B) { return (int64_t)(rows / 64) + B; }
 
+// The `blocks` records from c0 on lie among n_blocks of them; c0 is what a
+// table holds, any number.
+SQ_HD bool blocks_within(int32_t c0, int32_t blocks, int32_t n_blocks) { return c0 >= 0 && blocks <= n_blocks - c0; }
+// Number of block c among those from c0 on, negative where it is not one.
+SQ_HD int32_t block_after(int32_t c, int32_t c0) { return c0 < 0 || c0 > c ? -1 : c - c0; }
+
 }  // namespace sqr

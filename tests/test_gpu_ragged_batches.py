@@ -118,3 +118,20 @@ def test_workspace_of_too_many_requests_is_refused():
                 sp.ragged_workspace_bytes(B, 2 ** 30)
     finally:
         sp.close()
+
+
+@pytest.mark.parametrize("first", [2 ** 31 - 1, 2 ** 31 - 2, -1, -2 ** 31, 1000])
+def test_first_blocks_outside_the_workspace_are_skipped(first):
+    """A table entry that no call of sq_batch_tables writes: the request gets
+    o = 0, a status bit and no state, the others are right."""
+    bt = Batch([70, 200, 3, 64], past=[1, 0, 1, 1])
+    try:
+        bt.tables.cu_blocks[1] = first
+        bt.run()
+        check_rows(bt, skip=(1,))
+        assert (bt.o[70:270] == 0).all()
+        s = bt.slots[1]
+        assert torch.equal(bt.pool[s], bt.S0[s])
+        assert bt.h.get_status() == _abi.SQ_STATUS_BAD_SLOT
+    finally:
+        bt.close()

@@ -14,6 +14,10 @@ MAIN = r'''
 int main() {
   for (int32_t n : {0, 1, 63, (1 << 27) - 1, 1 << 27, 1 << 30}) std::printf("pieces %d %lld\n", n, (long long)sqr::row_pieces(n));
   for (int32_t b : {0, 1, 16384, 2147483647}) std::printf("blocks %d %lld\n", b, (long long)sqr::most_blocks(1 << 30, b));
+  for (int32_t c0 : {-2147483647 - 1, -1, 0, 7, 8, 2147483640, 2147483647}) {
+    std::printf("within %d %d\n", c0, (int)sqr::blocks_within(c0, 3, 10));
+    std::printf("after %d %d\n", c0, sqr::block_after(9, c0));
+  }
 }
 '''
 
@@ -40,3 +44,11 @@ def test_pieces_of_the_longest_request(lines):
 def test_blocks_of_the_largest_batch(lines):
     got = {int(b): int(n) for kind, b, n in (x for x in lines if x[0] == "blocks")}
     assert got == {b: 2 ** 24 + b for b in (0, 1, 16384, 2 ** 31 - 1)}
+
+
+def test_first_blocks_that_no_table_should_hold(lines):
+    """A first block near 2^31 must not pass as one inside the workspace."""
+    within = {int(c): bool(int(x)) for kind, c, x in (y for y in lines if y[0] == "within")}
+    after = {int(c): int(x) for kind, c, x in (y for y in lines if y[0] == "after")}
+    assert within == {c: 0 <= c <= 7 for c in within} and len(within) == 7
+    assert after == {c: 9 - c if 0 <= c <= 9 else -1 for c in after} and len(after) == 7
