@@ -23,11 +23,14 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _ptr(t: torch.Tensor | None, dtype=None, name="tensor", numel=None) -> int | None:
+def _ptr(t: torch.Tensor | None, dtype=None, name="tensor", numel=None, dev=None) -> int | None:
+    """Address of a contiguous CUDA tensor, on device `dev` where given (None passes)."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, not on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -123,10 +126,13 @@ class StatePool:
             return torch.zeros(self.pool_bytes, dtype=torch.uint8, device=self.device)
         return torch.zeros((self.n_slots, self.h_v, self.d, self.d), dtype=torch.float32, device=self.device)
 
+    def _arg(self, t, dtype=None, name="tensor", numel=None):
+        return _ptr(t, dtype, name, numel, self.device.index)
+
     def _check_pool(self, pool):
         if pool.numel() * pool.element_size() != self.pool_bytes:
             raise ValueError(f"pool has {pool.numel() * pool.element_size()} bytes, expected {self.pool_bytes}")
-        return _ptr(pool, name="pool")
+        return self._arg(pool, name="pool")
 
     def head_layout(self, head: int):
         return _abi.sq_head_layout(self._h, head)
@@ -139,18 +145,18 @@ class StatePool:
         B = S.shape[0]
         d, hv = self.d, self.h_v
         _abi.sq_quantize_state(self._h, self._check_pool(pool),
-                               _ptr(S, torch.float32, "S", B * hv * d * d),
-                               _ptr(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
+                               self._arg(S, torch.float32, "S", B * hv * d * d),
+                               self._arg(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
 
     def decode_step(self, pool, q, k, v, beta, g, o, slot_ids=None, stream=None):
         B = q.shape[0]
         d, hv, hk = self.d, self.h_v, self.h_k
         gn = B * hv * (d if self.gate_kind == _abi.SQ_GATE_KEY_CHANNEL else 1)
         _abi.sq_decode_step(self._h, self._check_pool(pool),
-                            _ptr(q, torch.float32, "q", B * hk * d), _ptr(k, torch.float32, "k", B * hk * d),
-                            _ptr(v, torch.float32, "v", B * hv * d), _ptr(beta, torch.float32, "beta", B * hv),
-                            _ptr(g, torch.float32, "g", gn), _ptr(o, torch.float32, "o", B * hv * d),
-                            _ptr(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
+                            self._arg(q, torch.float32, "q", B * hk * d), self._arg(k, torch.float32, "k", B * hk * d),
+                            self._arg(v, torch.float32, "v", B * hv * d), self._arg(beta, torch.float32, "beta", B * hv),
+                            self._arg(g, torch.float32, "g", gn), self._arg(o, torch.float32, "o", B * hv * d),
+                            self._arg(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
 
     def window_buffer_bytes(self, W: int):
         """(bytes of one (slot, head) window record, bytes of the whole buffer)."""
@@ -170,11 +176,11 @@ class StatePool:
         nb = self.window_buffer_bytes(W)[1]
         if wbuf.numel() * wbuf.element_size() != nb:
             raise ValueError(f"window buffer has {wbuf.numel() * wbuf.element_size()} bytes, expected {nb}")
-        _abi.sq_window_step(self._h, self._check_pool(pool), _ptr(wbuf, name="wbuf"), int(W),
-                            _ptr(q, torch.float32, "q", B * hk * d), _ptr(k, torch.float32, "k", B * hk * d),
-                            _ptr(v, torch.float32, "v", B * hv * d), _ptr(beta, torch.float32, "beta", B * hv),
-                            _ptr(g, torch.float32, "g", gn), _ptr(o, torch.float32, "o", B * hv * d),
-                            _ptr(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
+        _abi.sq_window_step(self._h, self._check_pool(pool), self._arg(wbuf, name="wbuf"), int(W),
+                            self._arg(q, torch.float32, "q", B * hk * d), self._arg(k, torch.float32, "k", B * hk * d),
+                            self._arg(v, torch.float32, "v", B * hv * d), self._arg(beta, torch.float32, "beta", B * hv),
+                            self._arg(g, torch.float32, "g", gn), self._arg(o, torch.float32, "o", B * hv * d),
+                            self._arg(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
 
     def decode_step_host(self, pool, q, k, v, beta, g, o, slot_ids=None, stream=None):
         """The decode step with q, k, v, beta, g, slot_ids and o as CPU tensors
@@ -200,12 +206,12 @@ class StatePool:
         d, hv, hk = self.d, self.h_v, self.h_k
         gn = B * L * hv * (d if self.gate_kind == _abi.SQ_GATE_KEY_CHANNEL else 1)
         n = B * L
-        _abi.sq_prefill(self._h, self._check_pool(pool), _ptr(S0, torch.float32, "S0", B * hv * d * d),
-                        _ptr(q, torch.float32, "q", n * hk * d), _ptr(k, torch.float32, "k", n * hk * d),
-                        _ptr(v, torch.float32, "v", n * hv * d), _ptr(beta, torch.float32, "beta", n * hv),
-                        _ptr(g, torch.float32, "g", gn), _ptr(o, torch.float32, "o", n * hv * d),
-                        _ptr(S_out, torch.float32, "S_out", B * hv * d * d),
-                        _ptr(lengths, torch.int32, "lengths", B), _ptr(slot_ids, torch.int32, "slot_ids", B),
+        _abi.sq_prefill(self._h, self._check_pool(pool), self._arg(S0, torch.float32, "S0", B * hv * d * d),
+                        self._arg(q, torch.float32, "q", n * hk * d), self._arg(k, torch.float32, "k", n * hk * d),
+                        self._arg(v, torch.float32, "v", n * hv * d), self._arg(beta, torch.float32, "beta", n * hv),
+                        self._arg(g, torch.float32, "g", gn), self._arg(o, torch.float32, "o", n * hv * d),
+                        self._arg(S_out, torch.float32, "S_out", B * hv * d * d),
+                        self._arg(lengths, torch.int32, "lengths", B), self._arg(slot_ids, torch.int32, "slot_ids", B),
                         B, L, _stream(stream))
 
     def ragged_workspace_bytes(self, B: int, rows: int, max_len: int | None = None, dtype=torch.bfloat16) -> int:
@@ -244,24 +250,24 @@ class StatePool:
                 with torch.cuda.stream(on):
                     workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         i32 = torch.int32
-        t = _abi.RaggedTables(_ptr(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
-                              _ptr(tables.cu_blocks, i32, "cu_blocks", B + 1),
-                              _ptr(tables.block_req, i32, "block_req"), _ptr(tables.past, i32, "past", B))
+        t = _abi.RaggedTables(self._arg(tables.cu_seqlens, i32, "cu_seqlens", B + 1),
+                              self._arg(tables.cu_blocks, i32, "cu_blocks", B + 1),
+                              self._arg(tables.block_req, i32, "block_req"), self._arg(tables.past, i32, "past", B))
         qp, qs = row_ptr(q, q.dtype, "q", rows, hk, d, dev)
         kp, ks = row_ptr(k, q.dtype, "k", rows, hk, d, dev)
         vp, vs = row_ptr(v, q.dtype, "v", rows, hv, d, dev)
         _abi.sq_prefill_ragged(self._h, self._check_pool(pool), qp, kp, vp, qs, ks, vs, DTYPES[q.dtype],
-                               _ptr(beta, torch.float32, "beta", rows * hv), _ptr(g, torch.float32, "g", gn),
-                               _ptr(o, q.dtype, "o", rows * hv * d), t, _ptr(slot_ids, i32, "slot_ids", B), B, rows,
-                               max_len, _ptr(workspace, torch.uint8, "workspace"),
+                               self._arg(beta, torch.float32, "beta", rows * hv), self._arg(g, torch.float32, "g", gn),
+                               self._arg(o, q.dtype, "o", rows * hv * d), t, self._arg(slot_ids, i32, "slot_ids", B), B, rows,
+                               max_len, self._arg(workspace, torch.uint8, "workspace"),
                                workspace.numel() if workspace is not None else 0, _raw_stream(stream, dev))
 
     def dequantize_state(self, pool, S_out, slot_ids=None, stream=None):
         B = S_out.shape[0]
         d, hv = self.d, self.h_v
         _abi.sq_dequantize_state(self._h, self._check_pool(pool),
-                                 _ptr(S_out, torch.float32, "S_out", B * hv * d * d),
-                                 _ptr(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
+                                 self._arg(S_out, torch.float32, "S_out", B * hv * d * d),
+                                 self._arg(slot_ids, torch.int32, "slot_ids", B), B, _stream(stream))
 
     def get_status(self, clear=True, stream=None) -> int:
         return _abi.sq_get_status(self._h, _stream(stream), clear)
