@@ -227,9 +227,10 @@ __device__ __forceinline__ void prepare_gates(PrepSmem& sm, uint8_t* rec, float2
   const bool on = which < heads;
   PrepGate& s = sm.gate[which];
   const float g = clamp_gate(gb.x), beta = gb.y;
-  // a gate of zero counts as 2^-126; a NaN stays one. log2f is good to an
+  // a gate of zero counts as 2^-128: pow2 makes 0 of every decay over it, as of
+  // those over a gate below 2^-126; a NaN stays one. log2f is good to an
   // ulp: over decays that matter the sum of those errors is below 2^-22.
-  float2 G = make_float2(log2f(g < 1.17549435e-38f ? 1.17549435e-38f : g), 0.0f);
+  float2 G = make_float2(g == 0.0f ? -128.0f : log2f(g), 0.0f);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const float2 y = make_float2(__shfl_up_sync(0xffffffffu, G.x, d), __shfl_up_sync(0xffffffffu, G.y, d));

@@ -1,10 +1,12 @@
 """GPU tests of ragged batches: calls that the documentation allows beside
 those of test_gpu_ragged.py."""
+import math
+
 import pytest
 import torch
 
 from quantized_linear_attention_sq_b200 import _abi
-from tests.test_gpu_ragged import Batch, check_rows, i32
+from tests.test_gpu_ragged import U, Batch, check_rows, i32, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -133,5 +135,30 @@ def test_first_blocks_outside_the_workspace_are_skipped(first):
         s = bt.slots[1]
         assert torch.equal(bt.pool[s], bt.S0[s])
         assert bt.h.get_status() == _abi.SQ_STATUS_BAD_SLOT
+    finally:
+        bt.close()
+
+
+@pytest.mark.parametrize("gate", [0.0, -1.0, 1e-40])
+@pytest.mark.parametrize("row", [0, 20, 63, 64])
+def test_a_gate_of_zero_forgets_the_largest_state(row, gate):
+    """Nothing of a state of 1e30 is left behind a gate of zero (or, at 1e-40,
+    1e-10 of it beside values of 1): not 2^-126 of it."""
+    def gates(g):
+        g[row] = gate
+    bt = Batch([100], past=[1], gates=gates, extra=0)
+    try:
+        if gate <= 0.0:
+            bt.v.mul_(1e-8)
+        bt.S0.mul_(1e30)
+        bt.pool.copy_(bt.S0)
+        bt.run()
+        (o, S), = bt.expected()
+        tol = 8 * U * math.sqrt(101)
+        assert rel(bt.pool[bt.slots[0]], S) <= tol
+        for r in (slice(0, row), slice(row, 100)):
+            if r.stop > r.start:
+                assert rel(bt.o[r].transpose(0, 1), o[r].transpose(0, 1)) <= 2.0 ** -8 + 4 * tol
+        assert bt.h.get_status() == 0
     finally:
         bt.close()
