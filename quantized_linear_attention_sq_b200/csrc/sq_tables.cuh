@@ -86,7 +86,7 @@ __device__ __forceinline__ void assign_slots(const TableArgs& a, uint16_t* list,
   constexpr int PER = 16;
   for (int s0 = 0; s0 < a.n_slots; s0 += kTabThreads * PER) {
     const int s = s0 + threadIdx.x * PER;
-    uint8_t f[PER];
+    alignas(16) uint8_t f[PER];
     int free_here = 0;
     if (s + PER <= a.n_slots && (reinterpret_cast<uintptr_t>(a.used) & 15u) == 0) {
       *reinterpret_cast<uint4*>(f) = *reinterpret_cast<const uint4*>(a.used + s);
