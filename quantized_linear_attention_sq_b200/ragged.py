@@ -43,18 +43,23 @@ def _device_of(t, name):
 
 
 def batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids=None, slot_used=None,
-                 slot_out=None, used_out=None, status=None, stream=None) -> None:
+                 slot_out=None, used_out=None, status=None, stream=None, max_rows=None) -> None:
     """Write the tables of a ragged batch (sq_batch_tables): lengths, past
     int32 [B] (past may be None), cu_seqlens, cu_blocks int32 [B + 1],
-    positions int32 [max_rows], block_req int32 [max_rows // 64 + B] or more.
+    positions int32 [max_rows], or None (max_rows is needed then),
+    block_req int32 [max_rows // 64 + B] or more.
     slot_ids, slot_out int32 [B] and slot_used, used_out uint8 [n_slots]: all
     four or none; requests with slot_ids < 0 take free slots."""
     dev = _device_of(lengths, "lengths")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slot_ids, slot_used,
-                                slot_out, used_out, status, stream)
-    B, rows = lengths.numel(), positions.numel()
+                                slot_out, used_out, status, stream, max_rows)
+    if max_rows is None:
+        if positions is None:
+            raise ValueError("max_rows is needed where positions is None")
+        max_rows = positions.numel()
+    B, rows = lengths.numel(), int(max_rows)
     if block_req.numel() < rows // BLOCK + B:
         raise ValueError(f"block_req has {block_req.numel()} elements, {rows // BLOCK + B} are needed")
     if not (slot_ids is None) == (slot_used is None) == (slot_out is None) == (used_out is None):
@@ -62,7 +67,7 @@ def batch_tables(lengths, past, cu_seqlens, cu_blocks, positions, block_req, slo
     n_slots = 0 if slot_used is None else slot_used.numel()
     _abi.sq_batch_tables(_arg(lengths, I32, "lengths", None, dev), _arg(past, I32, "past", B, dev), B, rows,
                          _arg(cu_seqlens, I32, "cu_seqlens", B + 1, dev), _arg(cu_blocks, I32, "cu_blocks", B + 1, dev),
-                         _arg(positions, I32, "positions", None, dev), _arg(block_req, I32, "block_req", None, dev),
+                         _arg(positions, I32, "positions", rows, dev), _arg(block_req, I32, "block_req", None, dev),
                          _arg(slot_ids, I32, "slot_ids", B, dev), _arg(slot_used, U8, "slot_used", None, dev), n_slots,
                          _arg(slot_out, I32, "slot_out", B, dev), _arg(used_out, U8, "used_out", n_slots, dev),
                          _arg(status, I32, "status", 1, dev), _raw_stream(stream, dev))
@@ -83,12 +88,14 @@ class BatchTables:
         z = lambda n: torch.zeros(n, dtype=torch.int32, device=device or torch.device("cuda"))  # noqa: E731
         return cls(z(B + 1), z(B + 1), z(max_rows // BLOCK + B), None, z(max_rows))
 
-    def build(self, lengths, past=None, slot_ids=None, slot_used=None, status=None, stream=None) -> "BatchTables":
+    def build(self, lengths, past=None, slot_ids=None, slot_used=None, status=None, stream=None,
+              max_rows=None) -> "BatchTables":
         """Fill the tables from lengths (int32 [B]); requests with slot_ids < 0
-        take free slots of the pool, in place in slot_ids and slot_used."""
+        take free slots of the pool, in place in slot_ids and slot_used.
+        max_rows: the batch's most rows, needed where there are no positions."""
         batch_tables(lengths, past, self.cu_seqlens, self.cu_blocks, self.positions, self.block_req,
                      slot_ids=slot_ids, slot_used=slot_used, slot_out=slot_ids, used_out=slot_used, status=status,
-                     stream=stream)
+                     stream=stream, max_rows=max_rows)
         self.past = past
         return self
 

@@ -162,3 +162,30 @@ def test_a_gate_of_zero_forgets_the_largest_state(row, gate):
         assert bt.h.get_status() == 0
     finally:
         bt.close()
+
+
+def test_tables_without_positions():
+    """The positions may be left out, as in the C call."""
+    from quantized_linear_attention_sq_b200.ragged import BatchTables, batch_tables
+    lengths, past = i32([5, 0, 130, 64, 9]), i32([1, 2, 3, 4, 5])
+    want = BatchTables.empty(5, 200).build(lengths, past)
+    t = BatchTables.empty(5, 200)
+    t.positions = None
+    t.build(lengths, past, max_rows=200)
+    for x in ("cu_seqlens", "cu_blocks", "block_req"):
+        assert torch.equal(getattr(t, x), getattr(want, x))
+    assert t.cu_seqlens.tolist() == [0, 5, 5, 135, 199, 200] and t.positions is None
+    with pytest.raises(ValueError, match="max_rows"):
+        t.build(lengths, past)
+    with pytest.raises(ValueError, match="block_req"):
+        t.build(lengths, past, max_rows=264)
+    with pytest.raises(ValueError, match="positions"):
+        batch_tables(lengths, past, want.cu_seqlens, want.cu_blocks, want.positions, want.block_req, max_rows=199)
+    # and a batch runs on such tables
+    bt = Batch([70, 1, 20])
+    try:
+        bt.tables.positions = None
+        bt.tables.build(i32(bt.lengths), i32(bt.past), max_rows=bt.rows)
+        check_rows(bt.run())
+    finally:
+        bt.close()
