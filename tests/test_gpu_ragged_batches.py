@@ -189,3 +189,38 @@ def test_tables_without_positions():
         check_rows(bt.run())
     finally:
         bt.close()
+
+
+def test_a_replay_beside_a_call_on_another_stream():
+    """A captured call replays while another handle's call runs on a side
+    stream, each with a workspace of its own; everything either reads is
+    ordered before both."""
+    lengths = [300, 1, 64, 129]
+    a, b = (Batch(lengths, hv=8, hk=4, seed=s) for s in (4, 5))
+    try:
+        ws = [x.h.new_ragged_workspace(x.B, x.rows) for x in (a, b)]
+        first = []
+        for x, w in zip((a, b), ws):
+            x.run(workspace=w)
+            check_rows(x)
+            first.append((x.o.clone(), x.pool.clone()))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            a.h.prefill_ragged(a.pool, a.q, a.k, a.v, a.beta, a.g, a.o, a.tables, slot_ids=a.slot_ids, workspace=ws[0])
+        side = torch.cuda.Stream()
+        for _ in range(20):
+            for x in (a, b):
+                x.pool.copy_(x.S0)
+                x.o.fill_(3.0)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                b.h.prefill_ragged(b.pool, b.q, b.k, b.v, b.beta, b.g, b.o, b.tables, slot_ids=b.slot_ids,
+                                   workspace=ws[1])
+            graph.replay()
+            torch.cuda.current_stream().wait_stream(side)
+            for x, (o, pool) in zip((a, b), first):
+                assert torch.equal(x.o, o) and torch.equal(x.pool, pool)
+        assert a.h.get_status() == 0 and b.h.get_status() == 0
+    finally:
+        a.close()
+        b.close()
