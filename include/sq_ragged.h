@@ -155,7 +155,12 @@ sq_status sq_prefill_ragged(sq_handle* h, void* pool, const void* q, const void*
                             int32_t rows, int32_t max_len, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace sq_prefill_ragged needs for these sizes (0 where it
- * needs none: workspace may then be NULL). Host only. */
+ * needs none: workspace may then be NULL). Where max_len lets requests run in
+ * blocks it is 31760 bytes for each of rows / 64 + B blocks and each value
+ * head, whether the blocks are used or not: with 32 value heads 1.1 GB for 32
+ * requests of 2048 rows, 4.2 GB for one of 262144, and 0.5 GB for 512 requests
+ * of one row if max_len does not say that they are short (it is 0 if it does).
+ * B may be at most SQ_RAGGED_MAX_REQUESTS (SQ_ERR_UNSUPPORTED beyond). Host only. */
 sq_status sq_ragged_workspace_bytes(const sq_handle* h, int32_t dtype, int32_t B, int32_t rows, int32_t max_len,
                                     uint64_t* bytes);
 

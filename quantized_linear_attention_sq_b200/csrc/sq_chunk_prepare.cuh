@@ -24,10 +24,10 @@
 // reaches it is held like the state's. Only the blocks on and below the diagonal
 // are stored, in the order the scan's matrix instructions read them.
 // Bound by latency: a value head is a chain of six short phases with a
-// barrier between them, and five CTAs per SM run theirs against each other: 485
-// us for 32 requests of 2048 rows with 32 value heads (594 us before five fitted
-// an SM). In 24 requests of 0..1900 rows a scheduler issues 0.47 instructions a
-// cycle.
+// barrier between them, and five CTAs per SM run theirs against each other: 534
+// us for 32 requests of 2048 rows with 32 value heads (485 us with two terms for
+// P T; from 594 to 521 when five fitted an SM). In 24 requests of 0..1900 rows a
+// scheduler issues 0.46 instructions a cycle.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -27,11 +27,13 @@
 // the next D1k; v and o pass between rows and tensor memory by ldmatrix and
 // stmatrix.
 // Bound by the latency of that chain: about 5.25 k cycles a block (32 requests
-// of 2048 rows with 32 heads: 710 us; one request of 32768 rows: 1422 us); in
-// 24 requests of 0..1900 rows the tensor pipe is active 40 % of the time and a
-// scheduler issues 0.48 instructions a cycle. With two terms for S the 32
+// of 2048 rows with 32 heads: 755 us; one request of 32768 rows: 1420 us); in
+// 24 requests of 0..1900 rows the tensor pipe is active 47 % of the time and a
+// scheduler issues 0.47 instructions a cycle. With two terms for S the 32
 // requests took 756 us where three took 822, but the state's error against 64
-// bits rose from 2.4e-7 to 1.0e-6: three stay.
+// bits rose from 2.4e-7 to 1.0e-6: three stay. Two terms for what only reaches
+// o took 710 us where three take 755, but values some 1000 times smaller than
+// those they overwrote came back 1 to 2 % off: three there too.
 #pragma once
 
 #include <cuda.h>
@@ -234,8 +236,10 @@ __device__ __forceinline__ void record_sync() { asm volatile("bar.sync 1, 256;" 
 
 // The request whose turn it is as the `rank`-th: of up to kRanked requests the
 // longest start first, so that no long one is left to run alone (24 requests
-// of 0..1900 rows: 146 us in their own order, 113 by length); with more
-// the order matters little and the search would take long.
+// of 0..1900 rows: 146 us in their own order, 113 by length). Each CTA sorts for
+// itself, which would take long with more: those run in their own order, and a
+// long request behind many short ones starts only after the short ones' CTAs,
+// which leave at once, have had their turns.
 __device__ __forceinline__ int request_of(const RaggedArgs& a, int rank, ScanCtl& ctl) {
   if (a.B > kRanked || a.B == 1) return rank;
   const int tid = threadIdx.x, padded = (a.B + 3) & ~3;

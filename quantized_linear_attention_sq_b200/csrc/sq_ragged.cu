@@ -135,7 +135,9 @@ cudaError_t launch_rows_gate(bool kda, int dtype, const sqr::RaggedArgs& a, cons
 // Requests of at least this many rows run in blocks on the tensor cores,
 // shorter ones row by row. Measured on 48 requests of 1..420 rows into 8-bit
 // states and on 24 of 0..1900 (the whole call, us): from 6 rows 276, 182; from
-// 10 rows 275, 180; from 16 rows 271, 190; from 24 rows 304, 212.
+// 10 rows 275, 180; from 16 rows 271, 190; from 24 rows 304, 212. Both have 32
+// value heads and were measured with two terms for o's operands; with few
+// heads, or with many requests of just over 10 rows, it was not measured.
 constexpr int kMinLong = 10;
 
 bool in_blocks(const sq_handle* h, int dtype, int32_t max_len) {

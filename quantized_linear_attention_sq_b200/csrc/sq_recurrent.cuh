@@ -17,7 +17,9 @@
 // single tokens with 32 heads take 365 us, 0.90 of the measured copy rate (385
 // before CTAs walked over tiles with copies under way). Many rows are bound by
 // the latency of the exchange: 128 requests of 1..6 rows with gates by key
-// channel take 118 us, 0.71 of it.
+// channel take 118 us, 0.71 of it. At two CTAs per SM a thread has 128 registers:
+// fp32 rows at D = 128 spill (head gates: 88 bytes stored, 172 loaded, 32 and 52
+// with packed states; channel gates: 28 and 40), 16-bit rows 4 and 8 bytes or none.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -230,7 +230,10 @@ class StatePool:
         [rows, h_k, d], v, o [rows, h_v, d] (bf16, fp16 or fp32; q, k and v may
         be column slices of wider matrices), beta [rows, h_v], g [rows, h_v]
         or [rows, h_v, d], tables a ragged.BatchTables. A request with
-        past > 0 goes on from its slot's state, another starts from zeros."""
+        past > 0 goes on from its slot's state, another starts from zeros.
+        max_len: the longest request's rows (by default all rows): a batch of
+        short requests that does not give it allocates the workspace of long
+        ones (ragged_workspace_bytes) and runs three kernels in place of one."""
         B, rows, d, hv, hk = tables.cu_seqlens.numel() - 1, q.shape[0], self.d, self.h_v, self.h_k
         if q.dtype not in DTYPES:
             raise ValueError(f"q must be one of {tuple(DTYPES)}, got {q.dtype}")
